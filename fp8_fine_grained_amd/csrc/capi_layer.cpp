@@ -1,0 +1,135 @@
+// C-ABI entry points declared in include/fp8fg_layer.h: argument validation on
+// the host, then the launches.  Validation runs before any HIP call.
+#include "fp8fg_layer.h"
+
+#include <cstdint>
+#include <limits>
+
+#include "launch.h"
+
+namespace {
+
+constexpr int64_t kInt32Max = std::numeric_limits<int32_t>::max();
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int64_t elem_size(int dtype) { return dtype == FP8FG_BF16 ? 2 : 4; }
+bool valid_dtype(int d) { return d == FP8FG_F32 || d == FP8FG_BF16; }
+int hip_status(hipError_t e) { return e == hipSuccess ? FP8FG_OK : FP8FG_ERR_HIP; }
+
+// A row-major operand of a norm call, `ld` elements between rows.
+int check_rows(const void* p, int dtype, int64_t H, int64_t ld) {
+  if (!p || ld < H) return FP8FG_ERR_INVALID_ARG;
+  if (ld > std::numeric_limits<int64_t>::max() / 16) return FP8FG_ERR_UNSUPPORTED;
+  if (!aligned(p, 16) || (ld * elem_size(dtype)) % 16 != 0) return FP8FG_ERR_MISALIGNED;
+  return FP8FG_OK;
+}
+
+int check_norm_sizes(int dtype, int w_dtype, int64_t M, int64_t H) {
+  if (!valid_dtype(dtype) || !valid_dtype(w_dtype) || M < 0 || H < 0) return FP8FG_ERR_INVALID_ARG;
+  if (H % 128 != 0 || H > fp8fg::kNormMaxH || M > kInt32Max) return FP8FG_ERR_UNSUPPORTED;
+  return FP8FG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8_add_rmsnorm_quant_1x128(const void* x, const void* residual, int dtype, int64_t M, int64_t H, int64_t ld_x,
+                                int64_t ld_r, const void* weight, int w_dtype, float eps, int pow2, void* h, void* y,
+                                uint8_t* q, float* scales, float* rstd, fp8fg_stream_t stream) {
+  int c = check_norm_sizes(dtype, w_dtype, M, H);
+  if (c != FP8FG_OK) return c;
+  if (!(eps >= 0.0f) || (pow2 != 0 && pow2 != 1)) return FP8FG_ERR_INVALID_ARG;
+  if (M == 0 || H == 0) return FP8FG_OK;
+  if ((c = check_rows(x, dtype, H, ld_x)) != FP8FG_OK) return c;
+  if (residual && (c = check_rows(residual, dtype, H, ld_r)) != FP8FG_OK) return c;
+  if (!weight || !q || !scales) return FP8FG_ERR_INVALID_ARG;
+  if (!aligned(weight, 16) || !aligned(h, 16) || !aligned(y, 16) || !aligned(q, 16) || !aligned(scales, 4) ||
+      !aligned(rstd, 4))
+    return FP8FG_ERR_MISALIGNED;
+  fp8fg::NormArgs a{};
+  a.x = x; a.r = residual; a.w = weight; a.h = h; a.y = y; a.q = q; a.scales = scales; a.rstd = rstd;
+  a.M = M; a.H = H; a.ld_x = ld_x; a.ld_r = ld_r; a.eps = eps;
+  a.bf16 = dtype == FP8FG_BF16; a.w_bf16 = w_dtype == FP8FG_BF16; a.pow2 = pow2 == 1;
+  return hip_status(fp8fg::launch_rmsnorm_quant(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t H) {
+  if (M < 0 || H < 0 || H > fp8fg::kNormMaxH) return 0;
+  return fp8fg::rmsnorm_backward_partials(M, H) * H * static_cast<int64_t>(sizeof(float));
+}
+
+int fp8_rmsnorm_backward(const void* dy, const void* h, const void* dh, int dtype, int64_t M, int64_t H, int64_t ld_dy,
+                         int64_t ld_h, int64_t ld_dh, const float* rstd, const void* weight, int w_dtype, void* dx,
+                         float* dw, void* workspace, int64_t workspace_bytes, fp8fg_stream_t stream) {
+  int c = check_norm_sizes(dtype, w_dtype, M, H);
+  if (c != FP8FG_OK) return c;
+  if (H == 0 || (M == 0 && !dw)) return FP8FG_OK;
+  if (dw) {
+    if (!aligned(dw, 16)) return FP8FG_ERR_MISALIGNED;
+    const int64_t need = fp8_rmsnorm_backward_workspace(M, H);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FP8FG_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return FP8FG_ERR_MISALIGNED;
+  }
+  if (M > 0) {
+    if ((c = check_rows(dy, dtype, H, ld_dy)) != FP8FG_OK || (c = check_rows(h, dtype, H, ld_h)) != FP8FG_OK) return c;
+    if (dh && (c = check_rows(dh, dtype, H, ld_dh)) != FP8FG_OK) return c;
+    if (!rstd || !weight || !dx) return FP8FG_ERR_INVALID_ARG;
+    if (!aligned(rstd, 4) || !aligned(weight, 16) || !aligned(dx, 16)) return FP8FG_ERR_MISALIGNED;
+  }
+  fp8fg::NormGradArgs a{};
+  a.dy = dy; a.h = h; a.dh = dh; a.rstd = rstd; a.w = weight; a.dx = dx;
+  a.partial = dw ? static_cast<float*>(workspace) : nullptr;
+  a.M = M; a.H = H; a.ld_dy = ld_dy; a.ld_h = ld_h; a.ld_dh = ld_dh;
+  a.bf16 = dtype == FP8FG_BF16; a.w_bf16 = w_dtype == FP8FG_BF16;
+  return hip_status(fp8fg::launch_rmsnorm_backward(a, dw, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int grad_norm(const void* const* grads, void* const* outs, bool clip, const int64_t* counts, const int* dtypes,
+              int64_t n, float max_norm, float* norm, void* workspace, int64_t workspace_bytes,
+              fp8fg_stream_t stream) {
+  if (n < 0 || !norm || (n > 0 && (!grads || !counts || !dtypes || (clip && !outs)))) return FP8FG_ERR_INVALID_ARG;
+  if (clip && !(max_norm > 0.0f)) return FP8FG_ERR_INVALID_ARG;
+  if (n > 0 && (!workspace || workspace_bytes < fp8fg_grad_norm_workspace(n))) return FP8FG_ERR_INVALID_ARG;
+  if (!aligned(norm, 4) || !aligned(workspace, 8)) return FP8FG_ERR_MISALIGNED;
+  // (120 tensors of 2^36 elements are 2^30 chunks of 8192: a launch numbers them with 32 bits)
+  constexpr int64_t kMostElements = int64_t(1) << 36;
+  for (int64_t i = 0; i < n; ++i) {
+    if (!valid_dtype(dtypes[i]) || counts[i] < 0) return FP8FG_ERR_INVALID_ARG;
+    if (counts[i] == 0) continue;
+    if (!grads[i] || (clip && !outs[i])) return FP8FG_ERR_INVALID_ARG;
+    if (counts[i] > kMostElements) return FP8FG_ERR_UNSUPPORTED;
+    const unsigned es = static_cast<unsigned>(elem_size(dtypes[i]));
+    if (!aligned(grads[i], es) || (clip && !aligned(outs[i], es))) return FP8FG_ERR_MISALIGNED;
+  }
+  fp8fg::GradList g{};
+  g.grads = grads; g.outs = clip ? outs : nullptr; g.counts = counts; g.dtypes = dtypes; g.n = n;
+  return hip_status(fp8fg::launch_grad_norm(g, max_norm, norm, static_cast<double*>(workspace),
+                                            static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8fg_grad_norm_workspace(int64_t n) {
+  if (n <= 0) return 0;
+  return (n + fp8fg::kGradBatch - 1) / fp8fg::kGradBatch * fp8fg::kGradPartials * static_cast<int64_t>(sizeof(double));
+}
+
+int fp8fg_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t n, float* norm,
+                    void* workspace, int64_t workspace_bytes, fp8fg_stream_t stream) {
+  return grad_norm(grads, nullptr, false, counts, dtypes, n, 0.0f, norm, workspace, workspace_bytes, stream);
+}
+
+int fp8fg_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes,
+                         int64_t n, float max_norm, float* norm, void* workspace, int64_t workspace_bytes,
+                         fp8fg_stream_t stream) {
+  return grad_norm(grads, outs, true, counts, dtypes, n, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -58,4 +58,49 @@ hipError_t launch_fp8_block_gemm(const GemmArgs& g, bool grouped, hipStream_t s)
 // (g.y_scales); requires N % 256 == 0, block-scaled B, FP8 or scaled accumulation.
 hipError_t launch_fp8_block_gemm_quant(const GemmArgs& g, bool pow2, hipStream_t s);
 
+// Residual addition, RMS norm and 1x128 quantisation (norm.hip).
+struct NormArgs {
+  const void* x;
+  const void* r;  // residual, or null
+  const void* w;
+  void* h;        // x + r in the input type, or null
+  void* y;        // the normed rows in the input type, or null
+  uint8_t* q;
+  float* scales;
+  float* rstd;    // or null
+  int64_t M, H, ld_x, ld_r;
+  float eps;
+  bool bf16, w_bf16, pow2;
+};
+hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t s);
+
+// Its gradient: dx, and the weight's gradient through per-workgroup partials
+// [rmsnorm_backward_partials(M, H), H].
+struct NormGradArgs {
+  const void* dy;
+  const void* h;
+  const void* dh;  // gradient arriving along the residual stream, or null
+  const float* rstd;
+  const void* w;
+  void* dx;
+  float* partial;  // null: no weight gradient
+  int64_t M, H, ld_dy, ld_h, ld_dh;
+  bool bf16, w_bf16;
+};
+constexpr int64_t kNormMaxH = 32768;  // a row stays in a workgroup's registers
+int64_t rmsnorm_backward_partials(int64_t M, int64_t H);
+hipError_t launch_rmsnorm_backward(const NormGradArgs& a, float* dw, hipStream_t s);
+
+// Global gradient norm and clipping (clip.hip).
+struct GradList {
+  const void* const* grads;
+  void* const* outs;  // null: norm only
+  const int64_t* counts;
+  const int* dtypes;
+  int64_t n;
+};
+constexpr int kGradBatch = 120;        // tensors per launch (kernel arguments)
+constexpr int kGradPartials = 1024;    // workgroups, hence partial sums, per launch
+hipError_t launch_grad_norm(const GradList& g, float max_norm, float* norm, double* partial, hipStream_t s);
+
 }  // namespace fp8fg

@@ -1,0 +1,98 @@
+/*
+ * fp8fg_layer -- the operators between the FP8 GEMMs of a feed-forward sublayer
+ * (training step and single-token serving), on gfx950.
+ *
+ * Same library, status codes, element types and conventions as fp8fg.h: device
+ * pointers unless stated otherwise, nothing allocated or retained, no
+ * synchronisation, every argument checked on the host before anything is
+ * enqueued, no exception across the boundary, capturable in a HIP graph.
+ * Workspaces are the caller's; a call's workspace may be reused once the stream
+ * has passed the call.  Outputs must not alias inputs unless stated otherwise.
+ */
+#ifndef FP8FG_LAYER_H
+#define FP8FG_LAYER_H
+
+#include "fp8fg.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Residual addition, root-mean-square norm and 1x128 quantisation, one pass:
+ *     z = x + residual                                (fp32)
+ *     rstd = 1 / sqrt(mean(z^2) + eps),  y = z * rstd * weight
+ *     q, scales = the 1x128 quantisation of y (rule of fp8_quant_act_1x128, or of
+ *                 fp8_quant_act_1x128_pow2 with pow2 == 1)
+ *     h = z rounded to `dtype`, for the residual stream and the backward pass.
+ * y comes from the unrounded z.  z^2 is summed in fp32, so |z| beyond about 1e19
+ * is outside the range; other finite inputs are fine.  A row of zeros gives zero
+ * codes and scales.
+ *
+ * x, residual  [M, H] of `dtype`, row pitches ld_x, ld_r >= H elements; residual
+ *              may be NULL (then z = x).
+ * weight       [H] of `w_dtype`.
+ * h            out [M, H] of `dtype`, or NULL.
+ * y            out [M, H] of `dtype` (y in high precision), or NULL.
+ * q, scales    out, codes [M, H] and fp32 [M, H/128].
+ * rstd         out, fp32 [M], or NULL.
+ * Requires H % 128 == 0 and H <= 32768; x, residual, weight, h, y and q 16-byte
+ * aligned, ld * sizeof(elem) % 16 == 0, scales and rstd 4-byte aligned; eps >= 0.
+ * M == 0 is a no-op.
+ */
+int fp8_add_rmsnorm_quant_1x128(const void* x, const void* residual, int dtype, int64_t M, int64_t H, int64_t ld_x,
+                                int64_t ld_r, const void* weight, int w_dtype, float eps, int pow2, void* h, void* y,
+                                uint8_t* q, float* scales, float* rstd, fp8fg_stream_t stream);
+
+/*
+ * Gradient of the norm (the quantisation passes gradients through unchanged):
+ * with n = h * rstd and d = dy * weight,
+ *     dx = rstd * (d - n * mean(d * n)) + dh,   dw = sum over rows of dy * n.
+ * dx is the gradient of both x and the residual.  dw is summed in fp32, in an
+ * order fixed by M and H alone: the same bits on every run.
+ *
+ * dy, h, dh    [M, H] of `dtype`, row pitches ld_* >= H; dh, the gradient that
+ *              arrives along the residual stream, may be NULL (zero).
+ * rstd         fp32 [M], as the forward call wrote it.
+ * weight       [H] of `w_dtype`.
+ * dx           out [M, H] of `dtype`.
+ * dw           out, fp32 [H], or NULL (then no workspace is needed).  Zero if M == 0.
+ * workspace    fp8_rmsnorm_backward_workspace(M, H) bytes, 16-byte aligned.
+ * Requirements as the forward call's.
+ */
+int fp8_rmsnorm_backward(const void* dy, const void* h, const void* dh, int dtype, int64_t M, int64_t H, int64_t ld_dy,
+                         int64_t ld_h, int64_t ld_dh, const float* rstd, const void* weight, int w_dtype, void* dx,
+                         float* dw, void* workspace, int64_t workspace_bytes, fp8fg_stream_t stream);
+int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t H);
+
+/*
+ * Global norm over n gradients:  norm = sqrt(sum of squares over all of them),
+ * squares summed in 64 bits, in an order fixed by the lengths alone.
+ *
+ * grads, counts, dtypes   HOST arrays of n device pointers, element counts (>= 0)
+ *              and element types; read during the call only.  A tensor of count
+ *              0 may have a null pointer.  Pointers need their element's alignment.
+ * norm         out, fp32 [1] (device).  Zero for n == 0.
+ * workspace    fp8fg_grad_norm_workspace(n) bytes, 8-byte aligned.
+ */
+int fp8fg_grad_norm(const void* const* grads, const int64_t* counts, const int* dtypes, int64_t n, float* norm,
+                    void* workspace, int64_t workspace_bytes, fp8fg_stream_t stream);
+
+/*
+ * The same norm, and every gradient scaled by
+ *     c = norm <= max_norm ? 1 : max_norm / norm
+ * (a norm that is not a number makes c, and so every output, not a number).
+ * outs         HOST array of n device pointers, of the gradients' types and
+ *              counts; outs[i] == grads[i] scales in place.
+ * Requires max_norm > 0.  Other arguments as fp8fg_grad_norm.
+ */
+int fp8fg_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes,
+                         int64_t n, float max_norm, float* norm, void* workspace, int64_t workspace_bytes,
+                         fp8fg_stream_t stream);
+int64_t fp8fg_grad_norm_workspace(int64_t n);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8FG_LAYER_H */
