@@ -89,6 +89,111 @@ int fp8_rmsnorm_backward(const void* dy, const void* h, const void* dh, int dtyp
 
 namespace {
 
+// Checks of a gated product and its launch arguments: FP8FG_OK, an error status,
+// or -1 when there is nothing to do.
+int check_gated(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, const void* h,
+                int h_dtype, const void* gu, int64_t M, int64_t I, int64_t K) {
+  if (!valid_dtype(h_dtype) || M < 0 || I < 0 || K < 0) return FP8FG_ERR_INVALID_ARG;
+  if (accum != FP8FG_ACCUM_FP8_MFMA && accum != FP8FG_ACCUM_EXACT && accum != FP8FG_ACCUM_SCALED_MFMA)
+    return FP8FG_ERR_INVALID_ARG;
+  if (M == 0 || I == 0) return -1;
+  if (K == 0 || K % 128 != 0 || I % 128 != 0) return FP8FG_ERR_UNSUPPORTED;
+  if (!a || !sa || !w || !sw || !h) return FP8FG_ERR_INVALID_ARG;
+  // (the tile loads' lane offsets are 32-bit: 256 rows of K bytes)
+  if (M > kInt32Max || I > kInt32Max / 2 || K >= (int64_t(1) << 24)) return FP8FG_ERR_UNSUPPORTED;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(h, 16) || !aligned(gu, 16) || !aligned(sa, 4) || !aligned(sw, 4))
+    return FP8FG_ERR_MISALIGNED;
+  return FP8FG_OK;
+}
+
+fp8fg::GemmArgs gated_args(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, void* h,
+                           int h_dtype, void* gu, int64_t M, int64_t I, int64_t K) {
+  fp8fg::GemmArgs g{};
+  g.a = a; g.sa = sa; g.b = w; g.sb = sw; g.y = h;
+  g.M = M; g.N = 2 * I; g.K = K; g.G = 1; g.T = M;
+  g.exact = accum == FP8FG_ACCUM_EXACT;
+  g.scaled = accum == FP8FG_ACCUM_SCALED_MFMA;
+  g.y_bf16 = h_dtype == FP8FG_BF16;
+  g.gu = gu;
+  return g;
+}
+
+int gated(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, void* h, int h_dtype,
+          float* s_h, int pow2, void* gu, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream) {
+  const int c = check_gated(a, sa, w, sw, accum, h, h_dtype, gu, M, I, K);
+  if (c != FP8FG_OK) return c < 0 ? FP8FG_OK : c;
+  if (((M + 127) / 128) * (I / 128) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;  // launch grid
+  fp8fg::GemmArgs g = gated_args(a, sa, w, sw, accum, h, h_dtype, gu, M, I, K);
+  g.y_scales = s_h;
+  g.pow2 = pow2 == 1;
+  return hip_status(fp8fg::launch_gated_gemm(g, static_cast<hipStream_t>(stream)));
+}
+
+int grouped_gated(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
+                  const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw, int accum, void* h,
+                  int h_dtype, float* s_h, int pow2, void* gu, int64_t M_total, int64_t I, int64_t K,
+                  fp8fg_stream_t stream) {
+  if (G < 0 || T < 0) return FP8FG_ERR_INVALID_ARG;
+  const int c = check_gated(a, sa, w, sw, accum, h, h_dtype, gu, M_total, I, K);
+  if (c > 0) return c;
+  if (c < 0 || G == 0) return FP8FG_OK;
+  if (T == 0 || !group_offsets || (!row_index && T != M_total)) return FP8FG_ERR_INVALID_ARG;
+  if (!aligned(group_offsets, 4) || !aligned(row_index, 4)) return FP8FG_ERR_MISALIGNED;
+  if (G > kInt32Max || (M_total / 128 + G) * (I / 128) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;
+  if (T > kInt32Max || T * K >= (int64_t(1) << 32)) return FP8FG_ERR_UNSUPPORTED;  // 32-bit row offsets
+  fp8fg::GemmArgs g = gated_args(a, sa, w, sw, accum, h, h_dtype, gu, M_total, I, K);
+  g.offsets = group_offsets;
+  g.row_index = row_index;
+  g.G = G;
+  g.T = T;
+  g.y_scales = s_h;
+  g.pow2 = pow2 == 1;
+  return hip_status(fp8fg::launch_gated_gemm(g, static_cast<hipStream_t>(stream)));
+}
+
+int check_quant_out(const float* s_h, int pow2, int64_t M, int64_t I) {
+  if (pow2 != 0 && pow2 != 1) return FP8FG_ERR_INVALID_ARG;
+  if (M > 0 && I > 0 && !s_h) return FP8FG_ERR_INVALID_ARG;
+  return aligned(s_h, 4) ? FP8FG_OK : FP8FG_ERR_MISALIGNED;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8_block_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, void* h,
+                         int h_dtype, void* gu, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream) {
+  return gated(a, sa, w, sw, accum, h, h_dtype, nullptr, 0, gu, M, I, K, stream);
+}
+
+int fp8_block_gated_gemm_quant(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum,
+                               int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M, int64_t I, int64_t K,
+                               fp8fg_stream_t stream) {
+  const int c = check_quant_out(s_h, pow2, M, I);
+  return c != FP8FG_OK ? c : gated(a, sa, w, sw, accum, q_h, FP8FG_BF16, s_h, pow2, gu, M, I, K, stream);
+}
+
+int fp8_block_grouped_gated_gemm(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
+                                 const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
+                                 int accum, void* h, int h_dtype, void* gu, int64_t M_total, int64_t I, int64_t K,
+                                 fp8fg_stream_t stream) {
+  return grouped_gated(a, sa, T, row_index, group_offsets, G, w, sw, accum, h, h_dtype, nullptr, 0, gu, M_total, I, K,
+                       stream);
+}
+
+int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
+                                       const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
+                                       int accum, int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M_total,
+                                       int64_t I, int64_t K, fp8fg_stream_t stream) {
+  const int c = check_quant_out(s_h, pow2, M_total, I);
+  return c != FP8FG_OK ? c : grouped_gated(a, sa, T, row_index, group_offsets, G, w, sw, accum, q_h, FP8FG_BF16, s_h,
+                                           pow2, gu, M_total, I, K, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
 int grad_norm(const void* const* grads, void* const* outs, bool clip, const int64_t* counts, const int* dtypes,
               int64_t n, float max_norm, float* norm, void* workspace, int64_t workspace_bytes,
               fp8fg_stream_t stream) {

@@ -93,6 +93,10 @@ struct FParams {
   // separate workgroups, which add their fp32 results into the zeroed output.
   int T_full;
   int split;
+  // Gated form only: where the gate and up values go (null: nowhere), and the
+  // scale form of a quantised output.
+  void* gu;
+  bool pow2;
 };
 
 // Dense tile order: bands of GROUP_M m-tiles, n-tile major inside a band, so the
@@ -156,6 +160,18 @@ __device__ __forceinline__ WideFrag widen(const v8i& f) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) w.q[q] = widen8(static_cast<uint32_t>(f[2 * q]), static_cast<uint32_t>(f[2 * q + 1]));
   return w;
+}
+
+// h = g * sigmoid(g) * u = g / (1 + exp(-g)) * u.  For g far below zero exp(-g)
+// overflows to infinity and the quotient is -0.  Outputs of the FP8 and scaled
+// sums carry the matrix cores' truncation (about 1e-4) and take the hardware
+// exponential and reciprocal (a few 1e-7); the exact sums the accurate ones.
+template <bool ACCURATE>
+__device__ __forceinline__ float gate_product(float g, float u) {
+  if constexpr (ACCURATE)
+    return g / (1.0f + expf(-g)) * u;
+  else
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // LDS DMA: 64 lanes x 16 bytes (or 4 bytes) to 1 KB (256 B) of LDS starting
@@ -227,9 +243,17 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // SCALED: power-of-two scales applied by the matrix cores (E8M0 operands of the
 // scaled MFMA), which also accumulate: no separate promotion step.
 // QOUT: the output leaves quantised, 1x128 along N, by the quantisers' rule
-// applied to the fp32 accumulators (1: scale amax/448, 2: power-of-two scale).
+// applied to the fp32 accumulators (1: scale amax/448, 2: power-of-two scale,
+// 3, gated form: either, by p.pow2).
+// GATED: B holds two stacked weights, gate rows 0 .. N/2-1 and up rows N/2 ..
+// N-1, and the output [M, N/2] is h = g * sigmoid(g) * u, formed in fp32 from
+// the accumulators.  A tile takes BN/2 output columns: each wavefront's n range
+// is TN/2 gate rows and the TN/2 up rows of the same columns, so that a lane
+// holds g and u of the same output elements and the product needs no exchange.
+// Only the source rows of the B tile, the promotion factors (one per half) and
+// the epilogue differ from the plain form.
 template <int BM, int BN, int WM, int WN, int STAGES, bool EXACT, bool ROWS, bool BF16OUT, bool GROUPED,
-          bool GATHER = false, bool SCALED = false, int QOUT = 0>
+          bool GATHER = false, bool SCALED = false, int QOUT = 0, bool GATED = false>
 __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams p) {
   constexpr int NW = WM * WN;  // wavefronts: 8 (2 per SIMD) or 4 (1 per SIMD)
   static_assert(NW == 8 || NW == 4, "8 or 4 wavefronts");
@@ -266,7 +290,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   static_assert(!(ROWS && GROUPED), "grouped weights carry block scales");
   static_assert(!GATHER || GROUPED, "gathering is a grouped-GEMM mode");
   static_assert(!SCALED || (!EXACT && !ROWS), "the scaled mode takes FP8 products and 128x128 weight scales");
-  static_assert(QOUT == 0 || (TN == 128 && BALIGN && !GROUPED), "a wavefront's row of the tile is one 1x128 group");
+  static_assert(QOUT == 0 || GATED || (TN == 128 && BALIGN && !GROUPED), "a wavefront's row of the tile is one 1x128 group");
+  constexpr int HALF = TN / 2;  // gated: a wavefront's output columns
+  static_assert(!GATED || (BN == 256 && !ROWS && !B_RR && SN % 2 == 0 && HALF % (BN / NW) == 0),
+                "gated tiles: 128 output columns (one 1x128 group), whole gate or up rows per wavefront's DMAs");
   // bf16 epilogue: each wavefront stages its TM x TN result (rows of TN*2 bytes
   // padded by 16) in its own slice of the tile buffer.
   constexpr int EPI_PITCH = TN * 2 + 16;
@@ -277,6 +304,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   __shared__ __attribute__((aligned(16))) float s_sb[STAGES][SB_LEN];
   __shared__ __attribute__((aligned(16))) float s_filler[64];  // landing slot of the filler DMAs, never read
   __shared__ int tile_info[4];
+  __shared__ float s_amax[GATED && QOUT != 0 ? WN * BM : 1];  // gated, quantised: row maxima of each wavefront column
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -416,6 +444,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     bscale += static_cast<int64_t>(g) * (p.N / 128) * p.KB;
   }
   const int64_t n0 = static_cast<int64_t>(nt) * BN;
+  // Row of B that tile row r (of BN) holds.
+  auto b_row = [&](int r) -> int64_t {
+    if constexpr (GATED)
+      return ((r / HALF) & 1) * (p.N / 2) + static_cast<int64_t>(nt) * (BN / 2) + (r / TN) * HALF + r % HALF;
+    else
+      return n0 + r;
+  };
 
   // ---- per-lane source addresses (rows fixed for the whole K loop).
   // Wavefront w fills A rows [w*BM/8, (w+1)*BM/8) and B rows [w*BN/8, ...),
@@ -429,6 +464,9 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   // Source row of A (and of its scales) for tile row `row` (in [row_lo, row_hi)).
   auto a_row = [&](int64_t row) -> int64_t {
     if constexpr (GATHER) {
+      if constexpr (GATED) {
+        if (!p.rows) return row;  // the gated grouped form takes the index or leaves it out
+      }
       int64_t t = p.rows[row];
       return t < 0 ? 0 : (t >= p.T ? p.T - 1 : t);
     } else {
@@ -442,7 +480,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   // are folded into the wave-uniform base.  Gathered rows keep one offset per DMA.
   const int uw = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint8_t* a_base = uniform_ptr(GATHER ? p.a : p.a + (row_lo + uw * (BM / NW)) * p.K);
-  const uint8_t* b_base = uniform_ptr(bmat + (n0 + uw * (B_RR ? 8 : BN / NW)) * p.K);
+  const uint8_t* b_base = uniform_ptr(bmat + b_row(uw * (B_RR ? 8 : BN / NW)) * p.K);
   const uint32_t voff = static_cast<uint32_t>(lrow * p.K + lchunk);
   uint32_t va[GATHER ? A_DMA : 1];
   uint64_t a_live[A_DMA];  // lanes whose tile row lies inside the segment (or the matrix)
@@ -454,6 +492,12 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     row = row < row_hi ? row : row_hi - 1;
     if constexpr (GATHER) va[i] = static_cast<uint32_t>(a_row(row) * p.K + lchunk);
   }
+  // Weight block whose scales lane `lane` of a scale DMA loads.
+  auto b_block = [&]() -> int64_t {
+    if constexpr (GATED) return nt + (lane == 0 ? 0 : p.N / 256);  // the gate block, then the up block
+    int64_t blk = n0 / 128 + (lane < NB - 1 ? lane : NB - 1);
+    return blk < p.N / 128 ? blk : p.N / 128 - 1;
+  };
   const float* gs;
   if (wave < SA_WAVES) {
     int64_t row = row_lo + wave * 64 + lane;
@@ -464,9 +508,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     w = w < SB_WAVES ? w : 0;  // filler wavefronts re-read the first weight rows' scales
     gs = bscale + (n0 + w * 64 + lane) * p.KB;
   } else {
-    int64_t blk = n0 / 128 + (lane < NB - 1 ? lane : NB - 1);
-    blk = blk < p.N / 128 ? blk : p.N / 128 - 1;
-    gs = bscale + blk * p.KB;
+    gs = bscale + b_block() * p.KB;
   }
   // wave-uniform LDS destinations (readfirstlane tells the compiler they are scalar)
   const int uwave = __builtin_amdgcn_readfirstlane(wave);
@@ -477,11 +519,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
                           : (b_scale_wave ? lds_addr(&s_sb[0][(uwave - SA_WAVES) * 64]) : lds_addr(s_filler));
   const uint32_t lds_s_step = uwave < SA_WAVES ? BM * 4 : (b_scale_wave ? SB_LEN * 4 : 0);
   const float* gsb = nullptr;  // weight-block scales of the extra scale DMA
-  if constexpr (SB_EXTRA) {
-    int64_t blk = n0 / 128 + (lane < NB - 1 ? lane : NB - 1);
-    blk = blk < p.N / 128 ? blk : p.N / 128 - 1;
-    gsb = bscale + blk * p.KB;
-  }
+  if constexpr (SB_EXTRA) gsb = bscale + b_block() * p.KB;
 
   // L2 prefetch (256 x 256 dense tiles): in iteration kb every wavefront touches
   // one dword of K block kb + PF_DIST in 96 / NW rows, so the lines are on their way
@@ -503,7 +541,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
       r = r < live ? r : live - 1;
       pf_ptr = p.a + (row_lo + r) * p.K;
     } else {
-      pf_ptr = bmat + (n0 + (mt % 4) * (BN / 4) + (slot - BM / 8) % (BN / 4)) * p.K;
+      if constexpr (GATED)
+        pf_ptr = bmat + b_row((mt % 4) * (BN / 4) + (slot - BM / 8) % (BN / 4)) * p.K;
+      else
+        pf_ptr = bmat + (n0 + (mt % 4) * (BN / 4) + (slot - BM / 8) % (BN / 4)) * p.K;
     }
   }
   auto prefetch = [&](int kb) {
@@ -579,6 +620,124 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   // (loads complete in order: waiting for all but the newest PF_PRO retires block 0's DMAs)
   wait_barrier<WAIT_N + PF_PRO>();  // block 0 resident
 
+  // ---- epilogue of the gated form: acc[i] and acc[i + SN/2] hold g and u of the
+  // same outputs, row m = j*16 + (lane & 15), columns i*16 + 4*(lane >> 4) ..+3 of
+  // the wavefront's HALF.
+  auto gated_epilogue = [&](auto smc, const int roff) __attribute__((always_inline)) {
+    constexpr int SMW = decltype(smc)::value;
+    constexpr int TMW = SMW * 16;
+    constexpr int SH = SN / 2;
+    const int64_t I = p.N / 2;
+    const int64_t col0 = static_cast<int64_t>(nt) * (BN / 2) + wn * HALF;  // first output column
+    uint8_t* epi = tiles + wave * TM * EPI_PITCH;  // the wavefront's own staging slice
+    // NC bf16 columns per row, given by at(i, j) for sub-tile i, staged as rows and
+    // written as whole row segments to put(row, column).
+    auto store_bf16 = [&](auto ncc, auto at, auto put) {
+      constexpr int NC = decltype(ncc)::value;
+      constexpr int PITCH = NC * 2 + 16;
+#pragma unroll
+      for (int j = 0; j < SMW; ++j)
+#pragma unroll
+        for (int i = 0; i < NC / 16; ++i) {
+          const v4f v = at(i, j);
+          *reinterpret_cast<u32x2*>(epi + (j * 16 + (lane & 15)) * PITCH + (i * 16 + 4 * (lane >> 4)) * 2) =
+              u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+        }
+      // (ds ops of one wavefront complete in order: no barrier needed here)
+      constexpr int LANES = NC / 8, RPP = 64 / LANES;  // 16-byte lanes per row, rows per pass
+#pragma unroll
+      for (int pass = 0; pass < TMW / RPP; ++pass) {
+        const int mr = pass * RPP + lane / LANES;
+        const int64_t m = row_lo + roff + mr;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(epi + mr * PITCH + (lane % LANES) * 16);
+        if (m < row_hi) *reinterpret_cast<u32x4*>(put(m, (lane % LANES) * 8)) = v;
+      }
+    };
+    if (p.gu) {
+      if constexpr (BF16OUT || QOUT != 0) {
+        auto* gu = static_cast<uint16_t*>(p.gu);
+        // (half by half: the staging slice holds TM rows of HALF columns with room to spare)
+        store_bf16(std::integral_constant<int, HALF>{}, [&](int i, int j) { return acc[i][j]; },
+                   [&](int64_t m, int c) { return gu + m * p.N + col0 + c; });
+        store_bf16(std::integral_constant<int, HALF>{}, [&](int i, int j) { return acc[i + SH][j]; },
+                   [&](int64_t m, int c) { return gu + m * p.N + I + col0 + c; });
+      } else {
+        float* gu = static_cast<float*>(p.gu);
+#pragma unroll
+        for (int j = 0; j < SMW; ++j) {
+          const int64_t m = row_lo + roff + j * 16 + (lane & 15);
+          if (m >= row_hi) continue;
+#pragma unroll
+          for (int i = 0; i < SN; ++i)
+            *reinterpret_cast<v4f*>(gu + m * p.N + (i / SH) * I + col0 + (i % SH) * 16 + 4 * (lane >> 4)) = acc[i][j];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < SMW; ++j)
+#pragma unroll
+      for (int i = 0; i < SH; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = gate_product<EXACT>(acc[i][j][r], acc[i + SH][j][r]);
+    if constexpr (QOUT != 0) {
+      // A row's 1x128 group is spread over the WN wavefront columns of the tile.
+      float am[SMW];
+#pragma unroll
+      for (int j = 0; j < SMW; ++j) {
+        am[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < SH; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) am[j] = fmaxf(am[j], fabsf(acc[i][j][r]));
+        am[j] = fmaxf(am[j], __shfl_xor(am[j], 16));
+        am[j] = fmaxf(am[j], __shfl_xor(am[j], 32));
+        if (lane < 16) s_amax[wn * BM + roff + j * 16 + lane] = am[j];
+      }
+      __syncthreads();
+      constexpr int QP = HALF + 16;  // staging pitch (bytes)
+#pragma unroll
+      for (int j = 0; j < SMW; ++j) {
+        const int mr = j * 16 + (lane & 15);
+        float a = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WN; ++w) a = fmaxf(a, s_amax[w * BM + roff + mr]);
+        float sc, inv;
+        if (p.pow2)
+          group_scale<true>(a, sc, inv);
+        else
+          group_scale<false>(a, sc, inv);
+#pragma unroll
+        for (int i = 0; i < SH; ++i)
+          *reinterpret_cast<uint32_t*>(epi + mr * QP + i * 16 + 4 * (lane >> 4)) =
+              cvt4(acc[i][j][0] * inv, acc[i][j][1] * inv, acc[i][j][2] * inv, acc[i][j][3] * inv);
+        const int64_t m = row_lo + roff + mr;
+        if (wn == 0 && lane < 16 && m < row_hi) p.ys[m * (I / 128) + nt] = sc;
+      }
+      constexpr int LANES = HALF / 16, RPP = 64 / LANES;
+      static_assert(16 % RPP == 0 || RPP % 16 == 0, "whole passes");
+#pragma unroll
+      for (int pass = 0; pass < (TMW + RPP - 1) / RPP; ++pass) {
+        const int mr = pass * RPP + lane / LANES;
+        const int64_t m = row_lo + roff + mr;
+        if (mr < TMW && m < row_hi)
+          *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p.y) + m * I + col0 + (lane % LANES) * 16) =
+              *reinterpret_cast<const u32x4*>(epi + mr * QP + (lane % LANES) * 16);
+      }
+    } else if constexpr (BF16OUT) {
+      store_bf16(std::integral_constant<int, HALF>{}, [&](int i, int j) { return acc[i][j]; },
+                 [&](int64_t m, int c) { return static_cast<uint16_t*>(p.y) + m * I + col0 + c; });
+    } else {
+#pragma unroll
+      for (int j = 0; j < SMW; ++j) {
+        const int64_t m = row_lo + roff + j * 16 + (lane & 15);
+        if (m >= row_hi) continue;
+#pragma unroll
+        for (int i = 0; i < SH; ++i)
+          *reinterpret_cast<v4f*>(static_cast<float*>(p.y) + m * I + col0 + i * 16 + 4 * (lane >> 4)) = acc[i][j];
+      }
+    }
+  };
+
   // Fragments of the current block: all m sub-tiles, the first n sub-tile, and
   // the per-column promotion factors sa[m,kb] * sb[nb,kb] (block mode) or sa[m,kb]
   // (row mode, where sb[n,kb] is read per n sub-tile); block 0 here, and the
@@ -608,6 +767,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     } else {
     v8i fm[SMW];
     float f[SMW];
+    float fu[SMW];  // gated: the factors of the up half (f: the gate half)
+    auto up_half = [](int i) { return GATED && i >= SN / 2; };
     // Grouped tiles read each n fragment two sub-tile steps ahead (fn1 holds the
     // next one): 2% faster on the MoE shape, where a step is 4 MFMAs; the dense
     // tiles read one step ahead (two ahead measured 1.5% slower with eight
@@ -617,10 +778,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     // Scaled mode: E8M0 codes (the fp32 exponent field) of the lane's act-row
     // scale in each m sub-tile, and of the wavefront's weight-block scale.
     int ex[SMW];
-    int ew = 0;
+    int ew = 0, ewu = 0;  // (ewu: gated, the up half's)
     auto e8m0 = [](float v) { return static_cast<int>((__float_as_uint(v) >> 23) & 0xFFu); };
     auto act_scale = [&](int st, int j) { return s_sa[st][roff + j * 16 + (lane & 15)]; };
-    auto wgt_scale = [&](int st) { return s_sb[st][((wn * TN) / 128) % SB_LEN]; };
+    auto wgt_scale = [&](int st) { return s_sb[st][GATED ? 0 : ((wn * TN) / 128) % SB_LEN]; };
     // acc += 2^(ew-127) * 2^(ex-127) * (128-K FP8 partial), in one instruction; MFMA
     // "A" is the weight fragment (scale per weight row), "B" the act fragment.
     auto mma_scaled = [](const v8i& wfrag, const v8i& afrag, const v4f& c, int ewv, int exv) {
@@ -631,7 +792,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
       if constexpr (ROWS || !BALIGN)
         return a;
       else
-        return a * s_sb[st][(wn * TN) / 128];
+        return a * s_sb[st][GATED ? 0 : (wn * TN) / 128];
+    };
+    auto factor_up = [&](int st, int j) {
+      if constexpr (GATED) return s_sa[st][roff + j * 16 + (lane & 15)] * s_sb[st][1];
+      return 0.0f;
     };
     // Unaligned weight tiles: the block scale of n sub-tile i (staged blocks start
     // at block n0/128).
@@ -665,6 +830,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
 #pragma unroll
       for (int j = 0; j < SMW; ++j) sa_v[j] = act_scale(st, j);
       const float sw_v = wgt_scale(st);
+      float su_v = 0.0f;
+      if constexpr (GATED) su_v = s_sb[st][1];
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < SMW; ++j) {
@@ -681,8 +848,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
           f[j] = sa_v[j] * sw_v;
         else
           f[j] = sa_v[j];
+        if constexpr (GATED && !SCALED) fu[j] = sa_v[j] * su_v;
       }
       if constexpr (SCALED) ew = e8m0(sw_v);
+      if constexpr (SCALED && GATED) ewu = e8m0(su_v);
       fn = n0;
       if constexpr (FD2) fn1 = n1;
     };
@@ -694,6 +863,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
       for (int j = 0; j < SMW; ++j) {
         fm[j] = frag(tA, roff + j * 16, lane);
         f[j] = factor(0, j);
+        if constexpr (GATED) fu[j] = factor_up(0, j);
       }
       fn = frag(tA + TILE_A, wn * TN, lane);
       if constexpr (FD2) fn1 = frag(tA + TILE_A, wn * TN + 16, lane);
@@ -807,7 +977,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
         }
         if constexpr (ROWS) sbr[i & 1] = row_scales(st, i);
         if constexpr (SCALED) {
-          const int ewi = BALIGN ? ew : e8m0(bsv(i));
+          const int ewi = BALIGN ? (up_half(i) ? ewu : ew) : e8m0(bsv(i));
 #pragma unroll
           for (int j = 0; j < SMW; ++j) {
             acc[i][j] = mma_scaled(fn, fm[j], acc[i][j], ewi, ex[j]);
@@ -824,7 +994,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
             dma_slot(i, j);
             if (i > 0) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[i - 1][j][r] = fmaf(P[(i - 1) & 1][j][r], f[j], acc[i - 1][j][r]);
+              for (int r = 0; r < 4; ++r) acc[i - 1][j][r] = fmaf(P[(i - 1) & 1][j][r], up_half(i - 1) ? fu[j] : f[j], acc[i - 1][j][r]);
             } else if (DEFER && kb > 0) {
 #pragma unroll
               for (int r = 0; r < 4; ++r)
@@ -851,7 +1021,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
             }
           }
           if (i > 0)
-            promote(acc[i - 1], P[(i - 1) & 1], f, sbr[(i - 1) & 1], bsv(i > 0 ? i - 1 : 0));
+            promote(acc[i - 1], P[(i - 1) & 1], up_half(i - 1) ? fu : f, sbr[(i - 1) & 1], bsv(i > 0 ? i - 1 : 0));
           else if (DEFER && kb > 0)
             promote(acc[SN - 1], P[(SN - 1) & 1], f_prev, sbr[(SN - 1) & 1], 0.0f);
         }
@@ -880,7 +1050,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
       wait_barrier<WAIT_N + (PF > 0 ? 1 : 0)>();
       st = st == STAGES - 1 ? 0 : st + 1;
       if constexpr (SCALED) {
-        const int ew_old = BALIGN ? ew : e8m0(bsv(SN - 1));
+        const int ew_old = BALIGN ? (GATED ? ewu : ew) : e8m0(bsv(SN - 1));
         const v8i fn_old = fn;
         int ex_old[SMW];
 #pragma unroll
@@ -890,7 +1060,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
       }
       float f_old[SMW];
 #pragma unroll
-      for (int j = 0; j < SMW; ++j) f_old[j] = f[j];
+      for (int j = 0; j < SMW; ++j) f_old[j] = GATED ? fu[j] : f[j];  // (steps SN - 2 and SN - 1)
       if constexpr (NFIRST) {
         const v8i fn_old = fn;
         const WideFrag none{};
@@ -905,6 +1075,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
           // (After the final block this reads a stage nobody uses; the values are dropped.)
           fm[j] = frag(tA, roff + j * 16, lane);
           f[j] = factor(st, j);
+          if constexpr (GATED) fu[j] = factor_up(st, j);
         }
         fn = frag(tA + TILE_A, wn * TN, lane);
         if constexpr (FD2) fn1 = frag(tA + TILE_A, wn * TN + 16, lane);
@@ -925,7 +1096,9 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
 
     // ---- epilogue: lane holds Y[m][n .. n+3], m = sub-tile column, n = 4 consecutive rows
     __syncthreads();  // every wavefront is done with the tile buffers
-    if constexpr (QOUT != 0) {
+    if constexpr (GATED) {
+      gated_epilogue(smc, roff);
+    } else if constexpr (QOUT != 0) {
       // The wavefront's 128 columns of a row are one 1x128 group.  Row m = j*16 +
       // (lane & 15) of sub-tile column j sits in lanes l, l^16, l^32, l^48, 32
       // values each: amax over the lane's values, then over those four lanes.

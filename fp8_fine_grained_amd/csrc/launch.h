@@ -45,6 +45,8 @@ struct GemmArgs {
   const int32_t* row_index = nullptr;  // grouped with gather: row r of A is a[row_index[r]]
   int64_t T = 0;                       // rows of a (and sa) when gathering
   float* y_scales = nullptr;           // quantised output: scales [M, N/128] (y = codes [M, N])
+  void* gu = nullptr;                  // gated: gate and up values [M, N] (of y's type; bf16 when quantised), or null
+  bool pow2 = false;                   // gated, quantised: power-of-two scales
 };
 hipError_t launch_block_gemm(const GemmArgs& g, hipStream_t s);
 hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t s);
@@ -57,6 +59,11 @@ hipError_t launch_fp8_block_gemm(const GemmArgs& g, bool grouped, hipStream_t s)
 // Dense GEMM writing its output as 1x128-quantised E4M3 codes (g.y) and scales
 // (g.y_scales); requires N % 256 == 0, block-scaled B, FP8 or scaled accumulation.
 hipError_t launch_fp8_block_gemm_quant(const GemmArgs& g, bool pow2, hipStream_t s);
+
+// Gated pair of products h = g * sigmoid(g) * u (gemm_gated.hip): b holds the N/2
+// gate rows and then the N/2 up rows, y is [M, N/2].  Grouped when g.offsets is
+// set (rows read through g.row_index, or in order when it is null).
+hipError_t launch_gated_gemm(const GemmArgs& g, hipStream_t s);
 
 // Residual addition, RMS norm and 1x128 quantisation (norm.hip).
 struct NormArgs {

@@ -282,7 +282,7 @@ hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t s) {
 
 int64_t rmsnorm_backward_partials(int64_t M, int64_t H) {
   int64_t p = 0;
-  with_shape(H, [&](auto wpr, auto) {
+  (void)with_shape(H, [&](auto wpr, auto) {
     constexpr int WPR = decltype(wpr)::value, SLOTS = grad_waves(WPR) / WPR;
     p = (M + SLOTS - 1) / SLOTS;
     return hipSuccess;

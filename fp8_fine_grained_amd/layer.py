@@ -13,7 +13,7 @@ import os
 import torch
 
 from . import binding
-from .binding import _check, _contig, _dtype_code, _on_gpu, _ptr, _stream
+from .binding import _accum_code, _check, _contig, _dtype_code, _on_gpu, _ptr, _stream
 
 HEADER = os.path.join(os.path.dirname(binding.HEADER), "fp8fg_layer.h")
 
@@ -23,6 +23,10 @@ _SIGS = {
     "fp8_add_rmsnorm_quant_1x128": ([_p, _p, _i, _l, _l, _l, _l, _p, _i, _f, _i, _p, _p, _p, _p, _p, _p], _i),
     "fp8_rmsnorm_backward": ([_p, _p, _p, _i, _l, _l, _l, _l, _l, _p, _p, _i, _p, _p, _p, _l, _p], _i),
     "fp8_rmsnorm_backward_workspace": ([_l, _l], _l),
+    "fp8_block_gated_gemm": ([_p, _p, _p, _p, _i, _p, _i, _p, _l, _l, _l, _p], _i),
+    "fp8_block_gated_gemm_quant": ([_p, _p, _p, _p, _i, _i, _p, _p, _p, _l, _l, _l, _p], _i),
+    "fp8_block_grouped_gated_gemm": ([_p, _p, _l, _p, _p, _l, _p, _p, _i, _p, _i, _p, _l, _l, _l, _p], _i),
+    "fp8_block_grouped_gated_gemm_quant": ([_p, _p, _l, _p, _p, _l, _p, _p, _i, _i, _p, _p, _p, _l, _l, _l, _p], _i),
     "fp8fg_grad_norm": ([_p, _p, _p, _l, _p, _p, _l, _p], _i),
     "fp8fg_clip_grad_norm": ([_p, _p, _p, _p, _l, _f, _p, _p, _l, _p], _i),
     "fp8fg_grad_norm_workspace": ([_l], _l),
@@ -136,6 +140,112 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
         _dtype_code(weight.dtype), _ptr(dx), _ptr(dw), _ptr(ws), nbytes, _stream(stream))
     _check("fp8_rmsnorm_backward", st)
     return dx, dw
+
+
+def _gated_operands(a, sa, w, sw, rows):
+    """Shapes of a gated product: (K, I) after checking operands against each other."""
+    _on_gpu(a, sa, w, sw)
+    _contig(a, sa, w, sw)
+    K, I2 = a.shape[1], w.shape[-2]
+    lead = tuple(w.shape[:-2])
+    _like("a", torch.uint8, (rows, K), a)
+    _like("sa", torch.float32, (rows, K // 128), sa)
+    _like("w", torch.uint8, lead + (I2, K), w)
+    if I2 % 256 != 0 or K % 128 != 0:  # (the library's own refusal, before a shape check could hide it)
+        raise binding.Fp8fgError("gated product", binding.ERR_UNSUPPORTED)
+    _like("sw", torch.float32, lead + (I2 // 128, K // 128), sw)
+    return K, I2 // 2
+
+
+def _gated_outputs(rows, inner, dtype, dev, h, gu, save):
+    h = torch.empty((rows, inner), dtype=dtype, device=dev) if h is None else h
+    if gu is None and save:
+        gu = torch.empty((rows, 2 * inner), dtype=dtype if dtype != torch.uint8 else torch.bfloat16, device=dev)
+    _on_gpu(h, gu)
+    _like("h", h.dtype if dtype != torch.uint8 else dtype, (rows, inner), h)
+    _like("gu", h.dtype if dtype != torch.uint8 else torch.bfloat16, (rows, 2 * inner), gu)
+    _contig(h, *([gu] if gu is not None else []))
+    return h, gu
+
+
+def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=None, gu=None, save=False,
+                         stream=None):
+    """h = g sigmoid(g) u [M, I] with g, u = deq(a) deq(w)^T, in one kernel.
+
+    ``w`` [2I, K] holds the gate rows, then the up rows; ``accum`` as in
+    :func:`binding.fp8_block_gemm`.  With ``save=True`` (or a ``gu`` buffer) also
+    g and u [M, 2I] for the backward pass: returns ``(h, gu)``, else ``h``."""
+    M = a.shape[0]
+    K, inner = _gated_operands(a, sa, w, sw, M)
+    h, gu = _gated_outputs(M, inner, out_dtype, a.device, h, gu, save)
+    st = lib().fp8_block_gated_gemm(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h),
+                                    _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream))
+    _check("fp8_block_gated_gemm", st)
+    return h if gu is None else (h, gu)
+
+
+def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, scales=None, gu=None, save=False,
+                               stream=None):
+    """The same with h leaving 1x128-quantised: ``(q uint8 [M, I], scales fp32 [M, I/128])``,
+    and the bf16 ``gu`` [M, 2I] as a third with ``save=True``."""
+    M = a.shape[0]
+    K, inner = _gated_operands(a, sa, w, sw, M)
+    q, gu = _gated_outputs(M, inner, torch.uint8, a.device, q, gu, save)
+    scales = torch.empty((M, inner // 128), dtype=torch.float32, device=a.device) if scales is None else scales
+    _on_gpu(scales)
+    _like("scales", torch.float32, (M, inner // 128), scales)
+    _contig(scales)
+    st = lib().fp8_block_gated_gemm_quant(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, torch.bfloat16),
+                                          1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), M, inner, K,
+                                          _stream(stream))
+    _check("fp8_block_gated_gemm_quant", st)
+    return (q, scales) if gu is None else (q, scales, gu)
+
+
+def _segments(a, offsets, w, row_index):
+    if w.dim() != 3 or offsets.dtype != torch.int32 or offsets.numel() != w.shape[0] + 1:
+        raise ValueError("w must be [G, 2I, K] and offsets int32 [G+1]")
+    _on_gpu(offsets, row_index)
+    _contig(offsets)
+    if row_index is None:
+        return a.shape[0]
+    if row_index.dtype != torch.int32 or row_index.dim() != 1:
+        raise ValueError("row_index must be int32 [M_total]")
+    _contig(row_index)
+    return row_index.numel()
+
+
+def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=None, out_dtype=torch.bfloat16, h=None,
+                                 gu=None, save=False, stream=None):
+    """The gated product over expert row segments ``offsets`` (device int32 [G+1]) with
+    weights ``w`` [G, 2I, K].  Row r is token ``row_index[r]`` of ``a`` [T, K], or row r
+    of ``a`` itself.  Returns ``h`` [M_total, I] (and ``gu``) in routed-row order."""
+    M = _segments(a, offsets, w, row_index)
+    K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
+    h, gu = _gated_outputs(M, inner, out_dtype, a.device, h, gu, save)
+    st = lib().fp8_block_grouped_gated_gemm(
+        _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw),
+        _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream))
+    _check("fp8_block_grouped_gated_gemm", st)
+    return h if gu is None else (h, gu)
+
+
+def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, accum="fp8", pow2=False, q=None,
+                                       scales=None, gu=None, save=False, stream=None):
+    """The same with h leaving 1x128-quantised: ``(q, scales)``, and ``gu`` with ``save=True``."""
+    M = _segments(a, offsets, w, row_index)
+    K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
+    q, gu = _gated_outputs(M, inner, torch.uint8, a.device, q, gu, save)
+    scales = torch.empty((M, inner // 128), dtype=torch.float32, device=a.device) if scales is None else scales
+    _on_gpu(scales)
+    _like("scales", torch.float32, (M, inner // 128), scales)
+    _contig(scales)
+    st = lib().fp8_block_grouped_gated_gemm_quant(
+        _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw),
+        _accum_code(accum, torch.bfloat16), 1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), M, inner, K,
+        _stream(stream))
+    _check("fp8_block_grouped_gated_gemm_quant", st)
+    return (q, scales) if gu is None else (q, scales, gu)
 
 
 def _grad_arrays(grads):

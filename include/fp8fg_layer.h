@@ -66,6 +66,51 @@ int fp8_rmsnorm_backward(const void* dy, const void* h, const void* dh, int dtyp
 int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t H);
 
 /*
+ * Gated pair of block-scaled FP8 products, with the activation and the product
+ * in the same kernel (the gate and up projections of a feed-forward block):
+ *     g = deq(A) deq(W[0:I])^T,  u = deq(A) deq(W[I:2I])^T    (fp8_block_gemm's sums)
+ *     h = g * sigmoid(g) * u                                  (fp32)
+ *
+ * a, sa        codes [M, K] and scales [M, K/128] (1x128).
+ * w, sw        codes [2I, K], gate rows first, and scales [2I/128, K/128]
+ *              (128x128): the quantisation of the two weights stacked.
+ * accum        FP8FG_ACCUM_FP8_MFMA, FP8FG_ACCUM_EXACT or FP8FG_ACCUM_SCALED_MFMA.
+ * h            out [M, I] of `h_dtype`.
+ * gu           out [M, 2I] of `h_dtype`, g then u, for the backward pass; or NULL.
+ * Requires K % 128 == 0 with 128 <= K < 2^24, I % 128 == 0; a, w, h, gu 16-byte
+ * aligned, scales 4-byte.  M == 0 or I == 0 is a no-op.
+ */
+int fp8_block_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, void* h,
+                         int h_dtype, void* gu, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream);
+
+/*
+ * The same with h leaving 1x128-quantised along I (rule of fp8_quant_act_1x128, or
+ * of fp8_quant_act_1x128_pow2 with pow2 == 1), ready for the down projection.
+ * q_h, s_h     out, codes [M, I] (16-byte aligned) and fp32 [M, I/128].
+ * gu           out, bf16 [M, 2I], or NULL.
+ */
+int fp8_block_gated_gemm_quant(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum,
+                               int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M, int64_t I, int64_t K,
+                               fp8fg_stream_t stream);
+
+/*
+ * The gated pair over expert row segments (offsets, rows and weights as
+ * fp8_block_grouped_gemm_gather): row r of segment e takes token row_index[r],
+ * or row r of A when row_index is NULL (then T must equal M_total).
+ * w, sw        codes [G, 2I, K] and scales [G, 2I/128, K/128].
+ * h, gu        out [M_total, I] and [M_total, 2I] (or NULL), in routed-row order.
+ * Requires T * K < 2^32; otherwise as the calls above and the grouped GEMM.
+ */
+int fp8_block_grouped_gated_gemm(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
+                                 const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
+                                 int accum, void* h, int h_dtype, void* gu, int64_t M_total, int64_t I, int64_t K,
+                                 fp8fg_stream_t stream);
+int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
+                                       const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
+                                       int accum, int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M_total,
+                                       int64_t I, int64_t K, fp8fg_stream_t stream);
+
+/*
  * Global norm over n gradients:  norm = sqrt(sum of squares over all of them),
  * squares summed in 64 bits, in an order fixed by the lengths alone.
  *

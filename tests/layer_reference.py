@@ -15,10 +15,10 @@ def e4m3_values(q):
     return q.cpu().view(torch.float8_e4m3fn).double()
 
 
-def check_quant(q, scales, ref, rel, pow2=False, what="", floor=0.0):
+def check_quant(q, scales, ref, rel, pow2=False, what="", floor=None):
     """Codes [M, K] and scales [M, K/128] against the 64-bit values ``ref`` that
     the kernel holds in fp32 to within ``rel`` of each value plus ``floor``
-    (absolute) before quantising.
+    [M, K] (absolute) before quantising.
 
     Scales: amax/448 to within rel, floor and two roundings, or the power of two
     whose range holds the amax.  Codes: the value times the kernel's own scale
@@ -28,7 +28,8 @@ def check_quant(q, scales, ref, rel, pow2=False, what="", floor=0.0):
     q, s = e4m3_values(q).view(M, K // 128, 128), scales.cpu().double()
     r = ref.cpu().double().view(M, K // 128, 128)
     amax = r.abs().amax(dim=2)
-    err = rel * amax + floor
+    fl = torch.zeros_like(r) if floor is None else floor.cpu().double().view(M, K // 128, 128)
+    err = rel * amax + fl.amax(dim=2)
     if pow2:
         nz = s > 0
         m, _ = torch.frexp(s[nz])
@@ -38,12 +39,13 @@ def check_quant(q, scales, ref, rel, pow2=False, what="", floor=0.0):
         assert torch.all(amax[~nz] <= err[~nz]), f"{what}: zero scale for a nonzero group"
     else:
         assert torch.all((s - amax / E4M3_MAX).abs() <= err / E4M3_MAX + 2 * U * s), f"{what}: scales"
-    v = r / torch.where(s > 0, s, torch.ones_like(s))[:, :, None]
-    _, e = torch.frexp(v)
-    # a value just below a power of two may round up into the next binade's step
-    _, e_up = torch.frexp(v.abs() * (1 + rel + 4 * U))
-    step = torch.exp2((torch.maximum(e, e_up) - 1).clamp(min=-6).double() - 3)
-    tol = step / 2 + v.abs() * (rel + 4 * U) + floor / torch.where(s > 0, s, torch.ones_like(s))[:, :, None]
+    safe = torch.where(s > 0, s, torch.ones_like(s))[:, :, None]
+    v = r / safe
+    off = v.abs() * (rel + 4 * U) + fl / safe  # how far the scaled value may be from v
+    # the step of the largest value it may be
+    _, e = torch.frexp(v.abs() + off)
+    step = torch.exp2((e - 1).clamp(min=-6).double() - 3)
+    tol = step / 2 + off
     bad = ((q - v).abs() > tol) & (s > 0)[:, :, None]
     assert not bad.any(), f"{what}: {int(bad.sum())} codes off, first {bad.nonzero()[:3].tolist()}"
     assert torch.all(q[s == 0] == 0), f"{what}: codes of a zero group"
@@ -57,3 +59,13 @@ def check_close(got, ref, rel, what, dtype=None, floor=0.0):
     bad = ~((g - r).abs() <= tol)
     assert not bad.any(), (f"{what}: {int(bad.sum())} values off, worst "
                            f"{float(((g - r).abs() / tol).nan_to_num(1e9).max()):.2f} of the bound")
+
+
+def silu(g):
+    return g * torch.sigmoid(g)
+
+
+def gated_bound(g, u, dg, du, rel):
+    """Bound of |h - silu(g) u| when g and u are off by at most dg and du and the
+    activation's own arithmetic is off by rel: |silu'| <= 1.1 everywhere."""
+    return 1.1 * u.abs() * dg + silu(g).abs() * du + 1.1 * dg * du + rel * (silu(g) * u).abs()
