@@ -190,6 +190,29 @@ int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_
                                            pow2, gu, M_total, I, K, stream);
 }
 
+int fp8_gated_backward_quant(const void* dh, const void* gu, int dtype, int64_t M, int64_t I, int64_t ld_dh, int pow2,
+                             uint8_t* q, float* s, uint8_t* q_t, float* s_t, uint8_t* q_ht, float* s_ht,
+                             fp8fg_stream_t stream) {
+  if (!valid_dtype(dtype) || M < 0 || I < 0 || (pow2 != 0 && pow2 != 1)) return FP8FG_ERR_INVALID_ARG;
+  if (!q != !s || !q_t != !s_t || !q_ht != !s_ht) return FP8FG_ERR_INVALID_ARG;  // half a pair
+  if (M == 0 || I == 0) return FP8FG_OK;
+  if (!q && !q_t && !q_ht) return FP8FG_ERR_INVALID_ARG;
+  if (I % 128 != 0 || ((q_t || q_ht) && M % 128 != 0)) return FP8FG_ERR_UNSUPPORTED;
+  // launch grids: one workgroup per 128 x 128 tile, or per 16 groups of a row
+  if (M > kInt32Max || I > kInt32Max || M * (I / 128) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;
+  const int c = check_rows(dh, dtype, I, ld_dh);
+  if (c != FP8FG_OK) return c;
+  if (!gu) return FP8FG_ERR_INVALID_ARG;
+  if (!aligned(gu, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(q_ht, 16) || !aligned(s, 4) ||
+      !aligned(s_t, 4) || !aligned(s_ht, 4))
+    return FP8FG_ERR_MISALIGNED;
+  fp8fg::GatedGradArgs a{};
+  a.dh = dh; a.gu = gu; a.q = q; a.s = s; a.q_t = q_t; a.s_t = s_t; a.q_ht = q_ht; a.s_ht = s_ht;
+  a.M = M; a.I = I; a.ld_dh = ld_dh;
+  a.bf16 = dtype == FP8FG_BF16; a.pow2 = pow2 == 1;
+  return hip_status(fp8fg::launch_gated_backward(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"
 
 namespace {

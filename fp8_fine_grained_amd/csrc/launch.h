@@ -65,6 +65,23 @@ hipError_t launch_fp8_block_gemm_quant(const GemmArgs& g, bool pow2, hipStream_t
 // set (rows read through g.row_index, or in order when it is null).
 hipError_t launch_gated_gemm(const GemmArgs& g, hipStream_t s);
 
+// Gradient of the gated activation, quantised along its columns (q, s), along
+// the tokens (q_t, s_t), and h along the tokens (q_ht, s_ht); each pair may be
+// null, the transposed ones need M % 128 == 0 (gated_backward.hip).
+struct GatedGradArgs {
+  const void* dh;
+  const void* gu;
+  uint8_t* q;
+  float* s;
+  uint8_t* q_t;
+  float* s_t;
+  uint8_t* q_ht;
+  float* s_ht;
+  int64_t M, I, ld_dh;
+  bool bf16, pow2;
+};
+hipError_t launch_gated_backward(const GatedGradArgs& a, hipStream_t s);
+
 // Residual addition, RMS norm and 1x128 quantisation (norm.hip).
 struct NormArgs {
   const void* x;

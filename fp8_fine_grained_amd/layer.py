@@ -27,6 +27,7 @@ _SIGS = {
     "fp8_block_gated_gemm_quant": ([_p, _p, _p, _p, _i, _i, _p, _p, _p, _l, _l, _l, _p], _i),
     "fp8_block_grouped_gated_gemm": ([_p, _p, _l, _p, _p, _l, _p, _p, _i, _p, _i, _p, _l, _l, _l, _p], _i),
     "fp8_block_grouped_gated_gemm_quant": ([_p, _p, _l, _p, _p, _l, _p, _p, _i, _i, _p, _p, _p, _l, _l, _l, _p], _i),
+    "fp8_gated_backward_quant": ([_p, _p, _i, _l, _l, _l, _i, _p, _p, _p, _p, _p, _p, _p], _i),
     "fp8fg_grad_norm": ([_p, _p, _p, _l, _p, _p, _l, _p], _i),
     "fp8fg_clip_grad_norm": ([_p, _p, _p, _p, _l, _f, _p, _p, _l, _p], _i),
     "fp8fg_grad_norm_workspace": ([_l], _l),
@@ -246,6 +247,36 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
         _stream(stream))
     _check("fp8_block_grouped_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
+
+
+def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_columns=True, stream=None):
+    """Gradient of the gated activation for ``dh`` [M, I] and the saved ``gu`` [M, 2I],
+    quantised as it is formed.  Returns ``(q, s, q_t, s_t, q_ht, s_ht)``:
+
+    ``rows``       q [M, 2I], s [M, 2I/128]: (dg, du), for the data gradient;
+    ``columns``    q_t [2I, M], s_t [2I, M/128]: transposed, for the weight gradient;
+    ``h_columns``  q_ht [I, M], s_ht [I, M/128]: h transposed, for the down
+                   projection's weight gradient.
+    A pair that is not asked for is (None, None)."""
+    _on_gpu(dh, gu)
+    _rows(dh)
+    _contig(gu)
+    M, inner = dh.shape
+    _like("gu", dh.dtype, (M, 2 * inner), gu)
+    if (columns or h_columns) and M % 128 != 0:  # (fewer than 128 tokens would allocate scales of no columns)
+        raise binding.Fp8fgError("fp8_gated_backward_quant", binding.ERR_UNSUPPORTED)
+
+    def pair(want, n, k):
+        if not want:
+            return None, None
+        return (torch.empty((n, k), dtype=torch.uint8, device=dh.device),
+                torch.empty((n, k // 128), dtype=torch.float32, device=dh.device))
+
+    out = (*pair(rows, M, 2 * inner), *pair(columns, 2 * inner, M), *pair(h_columns, inner, M))
+    st = lib().fp8_gated_backward_quant(_ptr(dh), _ptr(gu), _dtype_code(dh.dtype), M, inner, _ld(dh), 1 if pow2 else 0,
+                                        *[_ptr(t) for t in out], _stream(stream))
+    _check("fp8_gated_backward_quant", st)
+    return out
 
 
 def _grad_arrays(grads):

@@ -111,6 +111,31 @@ int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_
                                        int64_t I, int64_t K, fp8fg_stream_t stream);
 
 /*
+ * Gradient of the gated activation, quantised as it is formed.  With g, u the
+ * halves of gu and p = sigmoid(g) (fp32):
+ *     dg = dh u p (1 + g (1 - p)),   du = dh g p,   h = g p u
+ *     q, s        [M, 2I], [M, 2I/128]: (dg, du) 1x128-quantised along its columns;
+ *                 dX = fp8_block_gemm of it with the transposed weight codes of
+ *                 fp8_quant_weight_128x128_dual.
+ *     q_t, s_t    [2I, M], [2I, M/128]: its transpose, quantised along the tokens;
+ *                 dW of the gate and up weights = fp8_block_gemm (FP8FG_B_ROW_1x128)
+ *                 of it with the transposed quantisation of X.
+ *     q_ht, s_ht  [I, M], [I, M/128]: h transposed, quantised along the tokens, for
+ *                 the down projection's dW.
+ * Quantisation by the rule of fp8_quant_act_1x128, or of its _pow2 form.
+ *
+ * dh           [M, I] of `dtype`, row pitch ld_dh >= I.
+ * gu           [M, 2I] of `dtype`, as the forward call saved it.
+ * Each output pair may be NULL (both of it), but not all three.
+ * Requires I % 128 == 0, and M % 128 == 0 for the transposed pairs; dh, gu, q, q_t
+ * and q_ht 16-byte aligned, ld_dh * sizeof(elem) % 16 == 0, scales 4-byte.
+ * M == 0 or I == 0 is a no-op.
+ */
+int fp8_gated_backward_quant(const void* dh, const void* gu, int dtype, int64_t M, int64_t I, int64_t ld_dh, int pow2,
+                             uint8_t* q, float* s, uint8_t* q_t, float* s_t, uint8_t* q_ht, float* s_ht,
+                             fp8fg_stream_t stream);
+
+/*
  * Global norm over n gradients:  norm = sqrt(sum of squares over all of them),
  * squares summed in 64 bits, in an order fixed by the lengths alone.
  *

@@ -189,7 +189,121 @@ def test_same_bits_every_run_other_stream_and_graph(gpu):
             assert all(torch.equal(a, b) for a, b in zip(bufs, eager)), f"replay {k}"
 
 
+# ---------------------------------------------------------------- gradient
+# p = sigmoid(g) carries the exponential's and the division's error, at most 4 U of
+# p; 1 - p is then off by 4 U of p, which the factor 1 + g (1 - p) sees times |g|.
+# dg: six more roundings of products.  du and h: four.
+def _grad_reference(dh, gu):
+    n = dh.shape[1]
+    d, g, u = dh.double(), gu[:, :n].double(), gu[:, n:].double()
+    p = torch.sigmoid(g)
+    dg = d * u * p * (1 + g * (1 - p))
+    floor = (d * u).abs() * p * (U * (4 * g.abs() * p + 4 * (g * (1 - p)).abs() + 16))
+    return torch.cat([dg, d * g * p], 1), torch.cat([floor, 16 * U * (d * g * p).abs()], 1), g * p * u
+
+
+def _grad_inputs(M, inner, dtype, seed=0, pitch=0):
+    gen = torch.Generator().manual_seed(seed + M + inner)
+    dh = (torch.randn((M, inner + pitch), generator=gen) * 1e-3).to(dtype)
+    gu = (torch.randn((M, 2 * inner), generator=gen) * 1.7)
+    gu[torch.rand(gu.shape, generator=gen) < 0.001] *= 30
+    return dh, gu.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,inner", [(1, 128), (3, 384), (17, 128), (128, 128), (129, 256), (256, 384), (384, 640),
+                                     (1024, 1024)])
+def test_gradient(gpu, M, inner, dtype):
+    say(f"gated gradient {M}x{inner} {dtype}")
+    dh, gu = _grad_inputs(M, inner, dtype)
+    ref, floor, h = _grad_reference(dh, gu)
+    whole = M % 128 == 0
+    for pow2 in (False, True):
+        r = layer.fp8_gated_backward_quant(dh.to(gpu), gu.to(gpu), pow2=pow2, columns=whole, h_columns=whole)
+        check_quant(r[0], r[1], ref, 4 * U, pow2, "rows", floor)
+        if whole:
+            check_quant(r[2], r[3], ref.t().contiguous(), 4 * U, pow2, "columns", floor.t().contiguous())
+            check_quant(r[4], r[5], h.t().contiguous(), 20 * U, pow2, "h columns")
+            # any choice of outputs gives the same values
+            for want in ((True, False, False), (False, True, False), (False, False, True), (True, True, False)):
+                part = layer.fp8_gated_backward_quant(dh.to(gpu), gu.to(gpu), pow2=pow2, rows=want[0],
+                                                      columns=want[1], h_columns=want[2])
+                for k in range(6):
+                    assert (part[k] is None) == (not want[k // 2])
+                    assert part[k] is None or torch.equal(part[k], r[k]), f"{want} output {k}"
+        else:
+            assert r[2:] == (None,) * 4
+
+
+def test_gradient_strides_bounds_and_extremes(gpu):
+    """dh with a row pitch, gates where exp overflows or p rounds to 0 or 1, zero groups."""
+    M, inner = 128, 256
+    for dtype, pitch in ((torch.bfloat16, 8), (torch.float32, 4)):
+        dh, gu = _grad_inputs(M, inner, dtype, pitch=pitch)
+        gu[0, :inner] = 100.0
+        gu[1, :inner] = -100.0
+        gu[2, :inner] = -30.0
+        gu[3] = 0
+        dh[4] = 0
+        ref, floor, h = _grad_reference(dh[:, :inner], gu)
+        r = layer.fp8_gated_backward_quant(dh.to(gpu)[:, :inner], gu.to(gpu))
+        # (a group whose maximum lies below 448 * 2^-126 has unspecified codes)
+        live = ref.view(M, -1, 128).abs().amax(2).ge(448 * 2.0 ** -126).all(1)
+        assert int((~live).sum()) <= 3
+        check_quant(r[0][live.to(gpu)], r[1][live.to(gpu)], ref[live], 4 * U, False, "rows", floor[live])
+        check_quant(r[2], r[3], ref.t().contiguous(), 4 * U, False, "columns", floor.t().contiguous())
+        assert torch.all(r[1][4] == 0) and torch.all(r[0][4] & 0x7F == 0)
+
+
+def test_gradient_against_differences(gpu):
+    """The dequantised codes against central differences of the 64-bit activation:
+    within half an E4M3 step (1/16 of the value, or 2^-10 of the scale) and 1e-6."""
+    M, inner = 2, 128
+    dh, gu = _grad_inputs(M, inner, torch.float32)
+    dh = dh * 1e3
+    q, s = layer.fp8_gated_backward_quant(dh.to(gpu), gu.to(gpu), columns=False, h_columns=False)[:2]
+    s = s.cpu().double().repeat_interleave(128, 1)
+    got = q.cpu().view(torch.float8_e4m3fn).double() * s
+
+    def f(v):
+        return (dh.double() * silu(v[:, :inner]) * v[:, inner:]).sum()
+
+    step = 1e-5
+    for i, j in ((0, 3), (1, 100), (0, 128 + 9), (1, 255)):
+        e = torch.zeros_like(gu, dtype=torch.float64)
+        e[i, j] = step
+        num = float((f(gu.double() + e) - f(gu.double() - e)) / (2 * step))
+        assert abs(num - float(got[i, j])) <= abs(num) / 16 + 2.0 ** -10 * float(s[i, j]) + 1e-6
+
+
+def test_gradient_through_the_products(gpu):
+    """dX and dW of the pair from the quantised gradient and the library's GEMMs,
+    against the same products of the dequantised operands in 64 bits."""
+    M, inner, K = 128, 128, 256
+    gen = torch.Generator().manual_seed(9)
+    x, w = torch.randn((M, K), generator=gen).to(gpu), torch.randn((2 * inner, K), generator=gen).to(gpu) / 16
+    qx, sx = binding.fp8_quant_act_1x128(x)
+    qw, sw, qwt, swt = binding.fp8_quant_weight_128x128_dual(w)
+    dh, _ = _grad_inputs(M, inner, torch.float32)
+    _, gu = layer.fp8_block_gated_gemm(qx, sx, qw, sw, accum="exact", out_dtype=torch.float32, save=True)
+    q, s, qt, st, qht, sht = layer.fp8_gated_backward_quant(dh.to(gpu), gu)
+    dx = binding.fp8_block_gemm(q, s, qwt, swt, accum="exact", out_dtype=torch.float32)
+    qxt, sxt = binding.fp8_quant_act_1x128(x.t())
+    dw = binding.fp8_block_gemm(qt, st, qxt, sxt, b_scale_mode="row", accum="exact", out_dtype=torch.float32)
+    for got, a, b in ((dx, _dec(q, s, False), _dec(qwt, swt, True)), (dw, _dec(qt, st, False), _dec(qxt, sxt, False))):
+        ref, mag = a @ b.t(), a.abs() @ b.abs().t()
+        assert torch.all((got.cpu().double() - ref).abs() <= 32 * U * mag + 2.0 ** -140)
+
+
 def test_refusals(gpu):
+    with pytest.raises(binding.Fp8fgError) as e:
+        layer.fp8_gated_backward_quant(torch.zeros((5, 128), device=gpu), torch.zeros((5, 256), device=gpu))
+    assert e.value.status == binding.ERR_UNSUPPORTED  # transposed codes of 5 tokens
+    with pytest.raises(ValueError):
+        layer.fp8_gated_backward_quant(torch.zeros((5, 128), device=gpu), torch.zeros((5, 128), device=gpu))
+    with pytest.raises(ValueError):
+        layer.fp8_gated_backward_quant(torch.zeros((5, 128), device=gpu),
+                                       torch.zeros((5, 256), dtype=torch.bfloat16, device=gpu))
     qa, sa, qw, sw = _operands(gpu, 4, 128, 256, False)
     with pytest.raises(binding.Fp8fgError) as e:
         layer.fp8_block_gated_gemm(qa, sa, qw[:128].contiguous(), sw[:1].contiguous())

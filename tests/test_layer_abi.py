@@ -82,6 +82,72 @@ def test_norm_backward_validation(L):
     assert f(M=0, dw=NULL, dy=NULL) == fp8.OK  # nothing to write
 
 
+GATED = dict(a=GOOD, sa=GOOD, w=GOOD, sw=GOOD, accum=fp8.ACCUM_FP8_MFMA)
+SEGMENTS = dict(a=GOOD, sa=GOOD, T=32, idx=GOOD, off=GOOD, G=4, w=GOOD, sw=GOOD, accum=fp8.ACCUM_FP8_MFMA)
+PLAIN_OUT = dict(h=GOOD, dt=fp8.BF16, gu=GOOD, M=4, I=128, K=256, stream=NULL)
+QUANT_OUT = dict(pow2=0, h=GOOD, s=GOOD, gu=GOOD, M=4, I=128, K=256, stream=NULL)
+
+
+@pytest.mark.parametrize("fn,ok", [("fp8_block_gated_gemm", {**GATED, **PLAIN_OUT}),
+                                   ("fp8_block_gated_gemm_quant", {**GATED, **QUANT_OUT}),
+                                   ("fp8_block_grouped_gated_gemm", {**SEGMENTS, **PLAIN_OUT}),
+                                   ("fp8_block_grouped_gated_gemm_quant", {**SEGMENTS, **QUANT_OUT})])
+def test_gated_validation(L, fn, ok):
+    f = _caller(getattr(L, fn), ok)
+    assert f(accum=9) == fp8.ERR_INVALID_ARG
+    assert f(M=-1) == fp8.ERR_INVALID_ARG
+    assert f(I=-128) == fp8.ERR_INVALID_ARG
+    assert f(I=64) == fp8.ERR_UNSUPPORTED
+    assert f(K=0) == fp8.ERR_UNSUPPORTED
+    assert f(K=200) == fp8.ERR_UNSUPPORTED
+    assert f(K=1 << 24) == fp8.ERR_UNSUPPORTED
+    assert f(M=1 << 31) == fp8.ERR_UNSUPPORTED
+    assert f(I=1 << 30) == fp8.ERR_UNSUPPORTED
+    for k in ("a", "sa", "w", "sw", "h"):
+        assert f(**{k: NULL}) == fp8.ERR_INVALID_ARG
+    for k in ("a", "w", "h", "gu"):
+        assert f(**{k: BAD}) == fp8.ERR_MISALIGNED
+    assert f(sa=ctypes.c_void_p(0x10001)) == fp8.ERR_MISALIGNED
+    assert f(M=0, a=NULL) == fp8.OK
+    assert f(I=0, a=NULL) == fp8.OK
+    if "dt" in ok:
+        assert f(dt=5) == fp8.ERR_INVALID_ARG
+    else:
+        assert f(pow2=3) == fp8.ERR_INVALID_ARG
+        assert f(s=NULL) == fp8.ERR_INVALID_ARG
+        assert f(s=ODD) == fp8.ERR_MISALIGNED
+    if "off" in ok:
+        assert f(G=-1) == fp8.ERR_INVALID_ARG
+        assert f(T=-1) == fp8.ERR_INVALID_ARG
+        assert f(T=0) == fp8.ERR_INVALID_ARG
+        assert f(off=NULL) == fp8.ERR_INVALID_ARG
+        assert f(off=ODD) == fp8.ERR_MISALIGNED
+        assert f(idx=ODD) == fp8.ERR_MISALIGNED
+        assert f(idx=NULL) == fp8.ERR_INVALID_ARG  # rows in order need T == M_total
+        assert f(T=1 << 20, K=1 << 13) == fp8.ERR_UNSUPPORTED
+        assert f(G=0) == fp8.OK
+
+
+def test_gated_backward_validation(L):
+    f = _caller(L.fp8_gated_backward_quant, dict(dh=GOOD, gu=GOOD, dt=fp8.BF16, M=128, I=256, ld=256, pow2=0, q=GOOD,
+                                                 s=GOOD, qt=GOOD, st=GOOD, qht=GOOD, sht=GOOD, stream=NULL))
+    assert f(dt=4) == fp8.ERR_INVALID_ARG
+    assert f(M=-128) == fp8.ERR_INVALID_ARG
+    assert f(pow2=2) == fp8.ERR_INVALID_ARG
+    assert f(I=200, ld=200) == fp8.ERR_UNSUPPORTED
+    assert f(M=100) == fp8.ERR_UNSUPPORTED
+    assert f(ld=128) == fp8.ERR_INVALID_ARG
+    assert f(ld=260) == fp8.ERR_MISALIGNED
+    for k in ("dh", "gu", "q", "s", "qt", "st", "qht", "sht"):
+        assert f(**{k: NULL}) == fp8.ERR_INVALID_ARG  # an input, or half a pair
+    assert f(q=NULL, s=NULL, qt=NULL, st=NULL, qht=NULL, sht=NULL) == fp8.ERR_INVALID_ARG
+    for k in ("dh", "gu", "q", "qt", "qht"):
+        assert f(**{k: BAD}) == fp8.ERR_MISALIGNED
+    for k in ("s", "st", "sht"):
+        assert f(**{k: ODD}) == fp8.ERR_MISALIGNED
+    assert f(M=0, dh=NULL, gu=NULL) == fp8.OK
+
+
 def test_grad_norm_validation(L):
     need = L.fp8fg_grad_norm_workspace(2)
     assert need > 0 and L.fp8fg_grad_norm_workspace(0) == 0
