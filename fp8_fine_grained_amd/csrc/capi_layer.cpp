@@ -119,19 +119,19 @@ fp8fg::GemmArgs gated_args(const uint8_t* a, const float* sa, const uint8_t* w, 
 }
 
 int gated(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, void* h, int h_dtype,
-          float* s_h, int pow2, void* gu, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream) {
+          float* s_h, int pow2, void* gu, void* workspace, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream) {
   const int c = check_gated(a, sa, w, sw, accum, h, h_dtype, gu, M, I, K);
   if (c != FP8FG_OK) return c < 0 ? FP8FG_OK : c;
   if (((M + 127) / 128) * (I / 128) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;  // launch grid
   fp8fg::GemmArgs g = gated_args(a, sa, w, sw, accum, h, h_dtype, gu, M, I, K);
   g.y_scales = s_h;
   g.pow2 = pow2 == 1;
-  return hip_status(fp8fg::launch_gated_gemm(g, static_cast<hipStream_t>(stream)));
+  return hip_status(fp8fg::launch_gated_gemm(g, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 int grouped_gated(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
                   const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw, int accum, void* h,
-                  int h_dtype, float* s_h, int pow2, void* gu, int64_t M_total, int64_t I, int64_t K,
+                  int h_dtype, float* s_h, int pow2, void* gu, void* workspace, int64_t M_total, int64_t I, int64_t K,
                   fp8fg_stream_t stream) {
   if (G < 0 || T < 0) return FP8FG_ERR_INVALID_ARG;
   const int c = check_gated(a, sa, w, sw, accum, h, h_dtype, gu, M_total, I, K);
@@ -148,13 +148,16 @@ int grouped_gated(const uint8_t* a, const float* sa, int64_t T, const int32_t* r
   g.T = T;
   g.y_scales = s_h;
   g.pow2 = pow2 == 1;
-  return hip_status(fp8fg::launch_gated_gemm(g, static_cast<hipStream_t>(stream)));
+  return hip_status(fp8fg::launch_gated_gemm(g, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
-int check_quant_out(const float* s_h, int pow2, int64_t M, int64_t I) {
-  if (pow2 != 0 && pow2 != 1) return FP8FG_ERR_INVALID_ARG;
+// Checks of a quantised output; a workspace too small to be used becomes null.
+int check_quant_out(const float* s_h, int pow2, void*& workspace, int64_t bytes, int64_t M, int64_t I) {
+  if ((pow2 != 0 && pow2 != 1) || bytes < 0) return FP8FG_ERR_INVALID_ARG;
   if (M > 0 && I > 0 && !s_h) return FP8FG_ERR_INVALID_ARG;
-  return aligned(s_h, 4) ? FP8FG_OK : FP8FG_ERR_MISALIGNED;
+  if (!aligned(s_h, 4) || !aligned(workspace, 16)) return FP8FG_ERR_MISALIGNED;
+  if (M > 0 && I > 0 && bytes / 4 / I < M) workspace = nullptr;
+  return FP8FG_OK;
 }
 
 }  // namespace
@@ -163,31 +166,43 @@ extern "C" {
 
 int fp8_block_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, void* h,
                          int h_dtype, void* gu, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream) {
-  return gated(a, sa, w, sw, accum, h, h_dtype, nullptr, 0, gu, M, I, K, stream);
+  return gated(a, sa, w, sw, accum, h, h_dtype, nullptr, 0, gu, nullptr, M, I, K, stream);
 }
 
 int fp8_block_gated_gemm_quant(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum,
-                               int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M, int64_t I, int64_t K,
-                               fp8fg_stream_t stream) {
-  const int c = check_quant_out(s_h, pow2, M, I);
-  return c != FP8FG_OK ? c : gated(a, sa, w, sw, accum, q_h, FP8FG_BF16, s_h, pow2, gu, M, I, K, stream);
+                               int pow2, uint8_t* q_h, float* s_h, void* gu, void* workspace, int64_t workspace_bytes,
+                               int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream) {
+  const int c = check_quant_out(s_h, pow2, workspace, workspace_bytes, M, I);
+  return c != FP8FG_OK ? c : gated(a, sa, w, sw, accum, q_h, FP8FG_BF16, s_h, pow2, gu, workspace, M, I, K, stream);
+}
+
+int64_t fp8_block_gated_gemm_quant_workspace(int accum, int64_t M, int64_t I, int64_t K, int64_t G) {
+  if (M <= 0 || I <= 0 || K <= 0 || G < 0 || M > kInt32Max || I > kInt32Max / 2) return 0;
+  fp8fg::GemmArgs g = gated_args(nullptr, nullptr, nullptr, nullptr, accum, nullptr, FP8FG_BF16, nullptr, M, I, K);
+  const int32_t grouped = 0;
+  if (G > 0) {
+    g.G = G;
+    g.offsets = &grouped;  // (only whether it is set is looked at)
+  }
+  return fp8fg::gated_quant_takes_workspace(g) ? M * I * 4 : 0;
 }
 
 int fp8_block_grouped_gated_gemm(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
                                  const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
                                  int accum, void* h, int h_dtype, void* gu, int64_t M_total, int64_t I, int64_t K,
                                  fp8fg_stream_t stream) {
-  return grouped_gated(a, sa, T, row_index, group_offsets, G, w, sw, accum, h, h_dtype, nullptr, 0, gu, M_total, I, K,
-                       stream);
+  return grouped_gated(a, sa, T, row_index, group_offsets, G, w, sw, accum, h, h_dtype, nullptr, 0, gu, nullptr, M_total,
+                       I, K, stream);
 }
 
 int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
                                        const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
-                                       int accum, int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M_total,
-                                       int64_t I, int64_t K, fp8fg_stream_t stream) {
-  const int c = check_quant_out(s_h, pow2, M_total, I);
+                                       int accum, int pow2, uint8_t* q_h, float* s_h, void* gu, void* workspace,
+                                       int64_t workspace_bytes, int64_t M_total, int64_t I, int64_t K,
+                                       fp8fg_stream_t stream) {
+  const int c = check_quant_out(s_h, pow2, workspace, workspace_bytes, M_total, I);
   return c != FP8FG_OK ? c : grouped_gated(a, sa, T, row_index, group_offsets, G, w, sw, accum, q_h, FP8FG_BF16, s_h,
-                                           pow2, gu, M_total, I, K, stream);
+                                           pow2, gu, workspace, M_total, I, K, stream);
 }
 
 int fp8_gated_backward_quant(const void* dh, const void* gu, int dtype, int64_t M, int64_t I, int64_t ld_dh, int pow2,

@@ -22,6 +22,8 @@ __global__ void __launch_bounds__(256) zero_split_tiles_kernel(float* __restrict
   }
 }
 
+}  // namespace
+
 // Compute units of the current device, queried once per device.
 int device_cus() {
   static std::atomic<int> cache[64];
@@ -34,6 +36,8 @@ int device_cus() {
   }
   return v;
 }
+
+namespace {
 
 template <int CFG, bool EXACT, bool ROWS, bool BF16OUT, bool GROUPED, bool GATHER, bool SCALED, int QOUT = 0>
 hipError_t launch_cfg(const GemmArgs& g, hipStream_t s) {

@@ -97,6 +97,7 @@ struct FParams {
   // scale form of a quantised output.
   void* gu;
   bool pow2;
+  bool gu_bf16;  // gate and up values in bf16 whatever h's type (h then goes to be quantised)
 };
 
 // Dense tile order: bands of GROUP_M m-tiles, n-tile major inside a band, so the
@@ -553,13 +554,14 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   constexpr int ND = A_DMA + B_DMA;  // tile DMAs per wavefront per stage
   // The fp32-scale dense tiles with block scales issue each DMA right after
   // one MFMA (the interleaved issue described in the K loop).
-  constexpr bool ILV_DENSE = !GROUPED && !SCALED && !EXACT && !ROWS && BALIGN && NW == 8;
+  constexpr bool ILV_DENSE = !GROUPED && !SCALED && !EXACT && !ROWS && BALIGN && NW == 8 && SN >= 8;
   // Sub-tile steps that issue the DMAs: four of eight for those tiles (their
   // GEMM on 4096 x 7168 x 7168: 187.9 us over six steps, 185.7 over four, 185.3
   // over two, 188.7 in one), six of eight for the other 256 x 256 tiles, three
   // of four for the grouped ones (1.6% faster on the MoE shape than two, which
   // the row-scaled weight-gradient tiles keep: three is 1-8% slower there)
   constexpr int SPREAD = ILV_DENSE ? 4 : (SN >= 7 ? SN - 2 : (SN >= 4 ? (GROUPED ? SN - 1 : SN / 2) : SN));
+  static_assert(SPREAD < SN, "every tile DMA of a stage is issued before the stage's last step");
   auto dma_tile = [&](int d, int kb, int st) {
     const int64_t kof = static_cast<int64_t>(kb_begin + kb) * 128;
     const uint32_t so = static_cast<uint32_t>(st) * STAGE;

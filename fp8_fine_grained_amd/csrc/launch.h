@@ -46,6 +46,7 @@ struct GemmArgs {
   int64_t T = 0;                       // rows of a (and sa) when gathering
   float* y_scales = nullptr;           // quantised output: scales [M, N/128] (y = codes [M, N])
   void* gu = nullptr;                  // gated: gate and up values [M, N] (of y's type; bf16 when quantised), or null
+  bool gu_bf16 = false;                // gated: gu in bf16 although y is fp32
   bool pow2 = false;                   // gated, quantised: power-of-two scales
 };
 hipError_t launch_block_gemm(const GemmArgs& g, hipStream_t s);
@@ -62,8 +63,14 @@ hipError_t launch_fp8_block_gemm_quant(const GemmArgs& g, bool pow2, hipStream_t
 
 // Gated pair of products h = g * sigmoid(g) * u (gemm_gated.hip): b holds the N/2
 // gate rows and then the N/2 up rows, y is [M, N/2].  Grouped when g.offsets is
-// set (rows read through g.row_index, or in order when it is null).
-hipError_t launch_gated_gemm(const GemmArgs& g, hipStream_t s);
+// set (rows read through g.row_index, or in order when it is null).  workspace:
+// M * N/2 floats for a quantised output of few rows, or null (one kernel, slower
+// for few rows); gated_quant_takes_workspace: whether it would be used.
+hipError_t launch_gated_gemm(const GemmArgs& g, float* workspace, hipStream_t s);
+bool gated_quant_takes_workspace(const GemmArgs& g);
+
+// Compute units of the current device (0 if it cannot be asked).
+int device_cus();
 
 // Gradient of the gated activation, quantised along its columns (q, s), along
 // the tokens (q_t, s_t), and h along the tokens (q_ht, s_ht); each pair may be

@@ -24,9 +24,11 @@ _SIGS = {
     "fp8_rmsnorm_backward": ([_p, _p, _p, _i, _l, _l, _l, _l, _l, _p, _p, _i, _p, _p, _p, _l, _p], _i),
     "fp8_rmsnorm_backward_workspace": ([_l, _l], _l),
     "fp8_block_gated_gemm": ([_p, _p, _p, _p, _i, _p, _i, _p, _l, _l, _l, _p], _i),
-    "fp8_block_gated_gemm_quant": ([_p, _p, _p, _p, _i, _i, _p, _p, _p, _l, _l, _l, _p], _i),
+    "fp8_block_gated_gemm_quant": ([_p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _l, _l, _l, _l, _p], _i),
+    "fp8_block_gated_gemm_quant_workspace": ([_i, _l, _l, _l, _l], _l),
     "fp8_block_grouped_gated_gemm": ([_p, _p, _l, _p, _p, _l, _p, _p, _i, _p, _i, _p, _l, _l, _l, _p], _i),
-    "fp8_block_grouped_gated_gemm_quant": ([_p, _p, _l, _p, _p, _l, _p, _p, _i, _i, _p, _p, _p, _l, _l, _l, _p], _i),
+    "fp8_block_grouped_gated_gemm_quant": ([_p, _p, _l, _p, _p, _l, _p, _p, _i, _i, _p, _p, _p, _p, _l, _l, _l, _l,
+                                            _p], _i),
     "fp8_gated_backward_quant": ([_p, _p, _i, _l, _l, _l, _i, _p, _p, _p, _p, _p, _p, _p], _i),
     "fp8fg_grad_norm": ([_p, _p, _p, _l, _p, _p, _l, _p], _i),
     "fp8fg_clip_grad_norm": ([_p, _p, _p, _p, _l, _f, _p, _p, _l, _p], _i),
@@ -58,6 +60,8 @@ def _workspace(nbytes, given, device, stream):
         _on_gpu(given)
         _contig(given)
         return given, given.numel() * given.element_size()
+    if nbytes == 0:
+        return None, 0
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     if stream is not None:
         s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
@@ -186,7 +190,7 @@ def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=N
 
 
 def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, scales=None, gu=None, save=False,
-                               stream=None):
+                               workspace=None, stream=None):
     """The same with h leaving 1x128-quantised: ``(q uint8 [M, I], scales fp32 [M, I/128])``,
     and the bf16 ``gu`` [M, 2I] as a third with ``save=True``."""
     M = a.shape[0]
@@ -196,9 +200,10 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
     _on_gpu(scales)
     _like("scales", torch.float32, (M, inner // 128), scales)
     _contig(scales)
-    st = lib().fp8_block_gated_gemm_quant(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, torch.bfloat16),
-                                          1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), M, inner, K,
-                                          _stream(stream))
+    mode = _accum_code(accum, torch.bfloat16)
+    ws, nbytes = _workspace(lib().fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device, stream)
+    st = lib().fp8_block_gated_gemm_quant(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), mode, 1 if pow2 else 0, _ptr(q),
+                                          _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream))
     _check("fp8_block_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
 
@@ -232,7 +237,7 @@ def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=No
 
 
 def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, accum="fp8", pow2=False, q=None,
-                                       scales=None, gu=None, save=False, stream=None):
+                                       scales=None, gu=None, save=False, workspace=None, stream=None):
     """The same with h leaving 1x128-quantised: ``(q, scales)``, and ``gu`` with ``save=True``."""
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
@@ -241,10 +246,12 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
     _on_gpu(scales)
     _like("scales", torch.float32, (M, inner // 128), scales)
     _contig(scales)
+    mode = _accum_code(accum, torch.bfloat16)
+    ws, nbytes = _workspace(lib().fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, w.shape[0]), workspace,
+                            a.device, stream)
     st = lib().fp8_block_grouped_gated_gemm_quant(
-        _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw),
-        _accum_code(accum, torch.bfloat16), 1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), M, inner, K,
-        _stream(stream))
+        _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw), mode,
+        1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream))
     _check("fp8_block_grouped_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
 

@@ -88,10 +88,18 @@ int fp8_block_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, co
  * of fp8_quant_act_1x128_pow2 with pow2 == 1), ready for the down projection.
  * q_h, s_h     out, codes [M, I] (16-byte aligned) and fp32 [M, I/128].
  * gu           out, bf16 [M, 2I], or NULL.
+ * workspace    4 * M * I bytes, 16-byte aligned, or NULL.  With few rows the work is
+ *              spread over small tiles that hold no whole group: h then passes
+ *              through the workspace in fp32 and a second kernel quantises it.
+ *              Without one (or with a smaller one) one kernel does it all, several
+ *              times slower there.
+ * fp8_block_gated_gemm_quant_workspace: the bytes a call with these sizes would
+ * use, 0 for none (G: experts of the grouped form, 0 for the dense one).
  */
 int fp8_block_gated_gemm_quant(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum,
-                               int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M, int64_t I, int64_t K,
-                               fp8fg_stream_t stream);
+                               int pow2, uint8_t* q_h, float* s_h, void* gu, void* workspace, int64_t workspace_bytes,
+                               int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream);
+int64_t fp8_block_gated_gemm_quant_workspace(int accum, int64_t M, int64_t I, int64_t K, int64_t G);
 
 /*
  * The gated pair over expert row segments (offsets, rows and weights as
@@ -107,8 +115,9 @@ int fp8_block_grouped_gated_gemm(const uint8_t* a, const float* sa, int64_t T, c
                                  fp8fg_stream_t stream);
 int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,
                                        const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
-                                       int accum, int pow2, uint8_t* q_h, float* s_h, void* gu, int64_t M_total,
-                                       int64_t I, int64_t K, fp8fg_stream_t stream);
+                                       int accum, int pow2, uint8_t* q_h, float* s_h, void* gu, void* workspace,
+                                       int64_t workspace_bytes, int64_t M_total, int64_t I, int64_t K,
+                                       fp8fg_stream_t stream);
 
 /*
  * Gradient of the gated activation, quantised as it is formed.  With g, u the

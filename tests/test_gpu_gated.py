@@ -88,6 +88,29 @@ def test_dense(gpu, inner, K, accum):
             _check_all(ref, accum, gu=gq, quant=(q, s), pow2=pow2, what=what)
 
 
+@pytest.mark.parametrize("accum", ["fp8", "exact", "scaled"])
+@pytest.mark.parametrize("M,inner,K", [
+    (1, 1024, 2048), (9, 2048, 1024), (16, 8192, 256), (20, 2048, 512), (40, 4096, 512), (64, 8192, 384),
+    (100, 4096, 256), (130, 6144, 128), (300, 2048, 896), (513, 2048, 256), (1000, 4096, 128), (1030, 8192, 128)])
+def test_every_workgroup_shape(gpu, M, inner, K, accum):
+    """Sizes over which the choice of the workgroup's shape moves, checked on the
+    rows around its edges; the quantised form with and without its workspace."""
+    say(f"gated shapes {M}x{inner}x{K} {accum}")
+    qa, sa, qw, sw = _operands(gpu, M, inner, K, accum == "scaled")
+    h, gu = layer.fp8_block_gated_gemm(qa, sa, qw, sw, accum=accum, save=True)
+    f32 = layer.fp8_block_gated_gemm(qa, sa, qw, sw, accum=accum, out_dtype=torch.float32)
+    q, s, gq = layer.fp8_block_gated_gemm_quant(qa, sa, qw, sw, accum=accum, save=True)
+    none = torch.empty(0, dtype=torch.uint8, device=gpu)
+    q1, s1, g1 = layer.fp8_block_gated_gemm_quant(qa, sa, qw, sw, accum=accum, save=True, workspace=none)
+    rows = sorted({r for r in (0, 1, 15, 16, 17, 31, 32, 63, 64, 127, 128, 255, 256, M // 2, M - 2, M - 1)
+                   if 0 <= r < M})
+    ref = _reference(qa[rows], sa[rows], qw, sw, accum)
+    what = f"{M}x{inner}x{K} {accum}"
+    _check_all(ref, accum, h[rows], gu[rows], what=what)
+    _check_all(ref, accum, f32[rows], gq[rows], (q[rows], s[rows]), what=what + " f32/quant")
+    _check_all(ref, accum, gu=g1[rows], quant=(q1[rows], s1[rows]), what=what + " one kernel")
+
+
 def test_outputs_stay_in_their_buffers(gpu):
     for M, inner, K in ((1, 128, 256), (19, 256, 128), (130, 384, 256)):
         qa, sa, qw, sw = _operands(gpu, M, inner, K, False)
@@ -117,7 +140,7 @@ def _segments(counts):
 
 
 # (tokens, rows of each expert): empty first, last and middle experts, one row, tiles' edges, all rows on one expert
-SEGMENTS = [(1, [1]), (3, [0, 2, 0, 1]), (7, [5, 0, 0, 9, 1, 17]), (40, [0, 128, 129, 16, 0]), (300, [300, 0, 0]),
+SEGMENTS = [(1, [1]), (16, [1] * 40), (500, [9] * 200), (2000, [700, 0, 1300]), (3, [0, 2, 0, 1]), (7, [5, 0, 0, 9, 1, 17]), (40, [0, 128, 129, 16, 0]), (300, [300, 0, 0]),
             (64, [0] * 70 + [3] * 20 + [0] * 10), (20, [0, 0])]
 
 

@@ -85,7 +85,7 @@ def test_norm_backward_validation(L):
 GATED = dict(a=GOOD, sa=GOOD, w=GOOD, sw=GOOD, accum=fp8.ACCUM_FP8_MFMA)
 SEGMENTS = dict(a=GOOD, sa=GOOD, T=32, idx=GOOD, off=GOOD, G=4, w=GOOD, sw=GOOD, accum=fp8.ACCUM_FP8_MFMA)
 PLAIN_OUT = dict(h=GOOD, dt=fp8.BF16, gu=GOOD, M=4, I=128, K=256, stream=NULL)
-QUANT_OUT = dict(pow2=0, h=GOOD, s=GOOD, gu=GOOD, M=4, I=128, K=256, stream=NULL)
+QUANT_OUT = dict(pow2=0, h=GOOD, s=GOOD, gu=GOOD, ws=GOOD, bytes=1 << 20, M=4, I=128, K=256, stream=NULL)
 
 
 @pytest.mark.parametrize("fn,ok", [("fp8_block_gated_gemm", {**GATED, **PLAIN_OUT}),
@@ -116,6 +116,8 @@ def test_gated_validation(L, fn, ok):
         assert f(pow2=3) == fp8.ERR_INVALID_ARG
         assert f(s=NULL) == fp8.ERR_INVALID_ARG
         assert f(s=ODD) == fp8.ERR_MISALIGNED
+        assert f(ws=BAD) == fp8.ERR_MISALIGNED
+        assert f(bytes=-1) == fp8.ERR_INVALID_ARG
     if "off" in ok:
         assert f(G=-1) == fp8.ERR_INVALID_ARG
         assert f(T=-1) == fp8.ERR_INVALID_ARG
