@@ -9,11 +9,12 @@ is no fallback, and a refused call raises :class:`binding.Fp8fgError`.
 
 import ctypes
 import os
+from array import array
 
 import torch
 
 from . import binding
-from .binding import _accum_code, _check, _contig, _dtype_code, _on_gpu, _ptr, _stream
+from .binding import _accum_code, _check, _contig, _dtype_code, _on_gpu
 
 HEADER = os.path.join(os.path.dirname(binding.HEADER), "fp8fg_layer.h")
 
@@ -50,6 +51,23 @@ def lib():
     return _lib
 
 
+# A single token's kernels take a few microseconds, so the calls keep their host side
+# short: pointers and the stream go as plain integers, only what a caller passed
+# in is checked, and each output is one allocation.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without building the object
+
+
+def _stream(stream, t):
+    """The HIP stream of a call on tensor ``t``: ``stream``, or torch's current one."""
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _workspace(nbytes, given, device, stream):
     """``given``, or ``nbytes`` of fresh scratch memory.
 
@@ -84,7 +102,7 @@ def _ld(t):
 
 def _like(what, dtype, shape, *ts):
     for t in ts:
-        if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        if t is not None and (t.dtype != dtype or t.shape != shape):
             raise ValueError(f"{what} must be {dtype} {list(shape)}")
 
 
@@ -99,23 +117,26 @@ def fp8_add_rmsnorm_quant_1x128(x, weight, residual=None, eps=1e-6, pow2=False, 
     _on_gpu(x, weight, residual, h, y, q, scales, rstd)
     _rows(x, residual)
     M, H = x.shape
-    _like("residual, h and y", x.dtype, (M, H), residual, h, y)
-    if weight.dim() != 1 or weight.numel() != H or not weight.is_contiguous():
-        raise ValueError("weight must be contiguous [H]")
-    dev = x.device
-    if residual is not None and h is None:
-        h = torch.empty((M, H), dtype=x.dtype, device=dev)
-    q = torch.empty((M, H), dtype=torch.uint8, device=dev) if q is None else q
-    scales = torch.empty((M, H // 128), dtype=torch.float32, device=dev) if scales is None else scales
-    rstd = torch.empty(M, dtype=torch.float32, device=dev) if rstd is None else rstd
+    dt, dev = x.dtype, x.device
+    _like("residual, h and y", dt, (M, H), residual, h, y)
     _like("q", torch.uint8, (M, H), q)
     _like("scales", torch.float32, (M, H // 128), scales)
     _like("rstd", torch.float32, (M,), rstd)
-    _contig(*[t for t in (h, y, q, scales, rstd) if t is not None])
-    st = lib().fp8_add_rmsnorm_quant_1x128(
-        _ptr(x), _ptr(residual), _dtype_code(x.dtype), M, H, _ld(x), _ld(residual), _ptr(weight),
-        _dtype_code(weight.dtype), eps, 1 if pow2 else 0, _ptr(h), _ptr(y), _ptr(q), _ptr(scales), _ptr(rstd),
-        _stream(stream))
+    _contig(*[t for t in (weight, h, y, q, scales, rstd) if t is not None])
+    if weight.shape != (H,):
+        raise ValueError("weight must be contiguous [H]")
+    if residual is not None and h is None:
+        h = torch.empty((M, H), dtype=dt, device=dev)
+    if q is None:
+        q = torch.empty((M, H), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((M, H // 128), dtype=torch.float32, device=dev)
+    if rstd is None:
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    st = (_lib or lib()).fp8_add_rmsnorm_quant_1x128(
+        x.data_ptr(), _ptr(residual), _dtype_code(dt), M, H, _ld(x), _ld(residual), weight.data_ptr(),
+        _dtype_code(weight.dtype), eps, 1 if pow2 else 0, _ptr(h), _ptr(y), q.data_ptr(), scales.data_ptr(),
+        rstd.data_ptr(), _stream(stream, x))
     _check("fp8_add_rmsnorm_quant_1x128", st)
     return x if h is None else h, q, scales, rstd
 
@@ -131,18 +152,20 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
     _like("h, dh and dx", dy.dtype, (M, H), h, dh, dx)
     _like("rstd", torch.float32, (M,), rstd)
     _like("dw", torch.float32, (H,), dw)
-    if weight.dim() != 1 or weight.numel() != H:
-        raise ValueError("weight must be [H]")
-    dx = torch.empty((M, H), dtype=dy.dtype, device=dy.device) if dx is None else dx
+    _contig(*[t for t in (rstd, weight, dx, dw) if t is not None])
+    if weight.shape != (H,):
+        raise ValueError("weight must be contiguous [H]")
+    if dx is None:
+        dx = torch.empty((M, H), dtype=dy.dtype, device=dy.device)
     if dw is None and need_dw:
         dw = torch.empty(H, dtype=torch.float32, device=dy.device)
-    _contig(rstd, weight, dx, *([dw] if dw is not None else []))
+    L = _lib or lib()
     ws, nbytes = None, 0
     if dw is not None:
-        ws, nbytes = _workspace(lib().fp8_rmsnorm_backward_workspace(M, H), workspace, dy.device, stream)
-    st = lib().fp8_rmsnorm_backward(
-        _ptr(dy), _ptr(h), _ptr(dh), _dtype_code(dy.dtype), M, H, _ld(dy), _ld(h), _ld(dh), _ptr(rstd), _ptr(weight),
-        _dtype_code(weight.dtype), _ptr(dx), _ptr(dw), _ptr(ws), nbytes, _stream(stream))
+        ws, nbytes = _workspace(L.fp8_rmsnorm_backward_workspace(M, H), workspace, dy.device, stream)
+    st = L.fp8_rmsnorm_backward(
+        dy.data_ptr(), h.data_ptr(), _ptr(dh), _dtype_code(dy.dtype), M, H, _ld(dy), _ld(h), _ld(dh), rstd.data_ptr(),
+        weight.data_ptr(), _dtype_code(weight.dtype), dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, _stream(stream, dy))
     _check("fp8_rmsnorm_backward", st)
     return dx, dw
 
@@ -152,25 +175,40 @@ def _gated_operands(a, sa, w, sw, rows):
     _on_gpu(a, sa, w, sw)
     _contig(a, sa, w, sw)
     K, I2 = a.shape[1], w.shape[-2]
-    lead = tuple(w.shape[:-2])
+    lead = w.shape[:-2]
     _like("a", torch.uint8, (rows, K), a)
     _like("sa", torch.float32, (rows, K // 128), sa)
-    _like("w", torch.uint8, lead + (I2, K), w)
+    _like("w", torch.uint8, (*lead, I2, K), w)
     if I2 % 256 != 0 or K % 128 != 0:  # (the library's own refusal, before a shape check could hide it)
         raise binding.Fp8fgError("gated product", binding.ERR_UNSUPPORTED)
-    _like("sw", torch.float32, lead + (I2 // 128, K // 128), sw)
+    _like("sw", torch.float32, (*lead, I2 // 128, K // 128), sw)
     return K, I2 // 2
 
 
 def _gated_outputs(rows, inner, dtype, dev, h, gu, save):
-    h = torch.empty((rows, inner), dtype=dtype, device=dev) if h is None else h
-    if gu is None and save:
-        gu = torch.empty((rows, 2 * inner), dtype=dtype if dtype != torch.uint8 else torch.bfloat16, device=dev)
-    _on_gpu(h, gu)
-    _like("h", h.dtype if dtype != torch.uint8 else dtype, (rows, inner), h)
-    _like("gu", h.dtype if dtype != torch.uint8 else torch.bfloat16, (rows, 2 * inner), gu)
-    _contig(h, *([gu] if gu is not None else []))
+    if h is None:
+        h = torch.empty((rows, inner), dtype=dtype, device=dev)
+    else:
+        _on_gpu(h)
+        _like("h", h.dtype if dtype != torch.uint8 else dtype, (rows, inner), h)
+        _contig(h)
+    gu_dtype = torch.bfloat16 if dtype == torch.uint8 else h.dtype
+    if gu is not None:
+        _on_gpu(gu)
+        _like("gu", gu_dtype, (rows, 2 * inner), gu)
+        _contig(gu)
+    elif save:
+        gu = torch.empty((rows, 2 * inner), dtype=gu_dtype, device=dev)
     return h, gu
+
+
+def _scales_out(rows, inner, dev, scales):
+    if scales is None:
+        return torch.empty((rows, inner // 128), dtype=torch.float32, device=dev)
+    _on_gpu(scales)
+    _like("scales", torch.float32, (rows, inner // 128), scales)
+    _contig(scales)
+    return scales
 
 
 def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=None, gu=None, save=False,
@@ -183,8 +221,8 @@ def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=N
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw, M)
     h, gu = _gated_outputs(M, inner, out_dtype, a.device, h, gu, save)
-    st = lib().fp8_block_gated_gemm(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h),
-                                    _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream))
+    st = (_lib or lib()).fp8_block_gated_gemm(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h),
+                                    _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream, a))
     _check("fp8_block_gated_gemm", st)
     return h if gu is None else (h, gu)
 
@@ -196,14 +234,11 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw, M)
     q, gu = _gated_outputs(M, inner, torch.uint8, a.device, q, gu, save)
-    scales = torch.empty((M, inner // 128), dtype=torch.float32, device=a.device) if scales is None else scales
-    _on_gpu(scales)
-    _like("scales", torch.float32, (M, inner // 128), scales)
-    _contig(scales)
+    scales = _scales_out(M, inner, a.device, scales)
     mode = _accum_code(accum, torch.bfloat16)
-    ws, nbytes = _workspace(lib().fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device, stream)
-    st = lib().fp8_block_gated_gemm_quant(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), mode, 1 if pow2 else 0, _ptr(q),
-                                          _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream))
+    ws, nbytes = _workspace((_lib or lib()).fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device, stream)
+    st = (_lib or lib()).fp8_block_gated_gemm_quant(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), mode, 1 if pow2 else 0, _ptr(q),
+                                          _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream, a))
     _check("fp8_block_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
 
@@ -229,9 +264,9 @@ def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=No
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
     h, gu = _gated_outputs(M, inner, out_dtype, a.device, h, gu, save)
-    st = lib().fp8_block_grouped_gated_gemm(
+    st = (_lib or lib()).fp8_block_grouped_gated_gemm(
         _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw),
-        _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream))
+        _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream, a))
     _check("fp8_block_grouped_gated_gemm", st)
     return h if gu is None else (h, gu)
 
@@ -242,16 +277,13 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
     q, gu = _gated_outputs(M, inner, torch.uint8, a.device, q, gu, save)
-    scales = torch.empty((M, inner // 128), dtype=torch.float32, device=a.device) if scales is None else scales
-    _on_gpu(scales)
-    _like("scales", torch.float32, (M, inner // 128), scales)
-    _contig(scales)
+    scales = _scales_out(M, inner, a.device, scales)
     mode = _accum_code(accum, torch.bfloat16)
-    ws, nbytes = _workspace(lib().fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, w.shape[0]), workspace,
+    ws, nbytes = _workspace((_lib or lib()).fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, w.shape[0]), workspace,
                             a.device, stream)
-    st = lib().fp8_block_grouped_gated_gemm_quant(
+    st = (_lib or lib()).fp8_block_grouped_gated_gemm_quant(
         _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw), mode,
-        1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream))
+        1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream, a))
     _check("fp8_block_grouped_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
 
@@ -280,33 +312,53 @@ def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_colu
                 torch.empty((n, k // 128), dtype=torch.float32, device=dh.device))
 
     out = (*pair(rows, M, 2 * inner), *pair(columns, 2 * inner, M), *pair(h_columns, inner, M))
-    st = lib().fp8_gated_backward_quant(_ptr(dh), _ptr(gu), _dtype_code(dh.dtype), M, inner, _ld(dh), 1 if pow2 else 0,
-                                        *[_ptr(t) for t in out], _stream(stream))
+    st = (_lib or lib()).fp8_gated_backward_quant(_ptr(dh), _ptr(gu), _dtype_code(dh.dtype), M, inner, _ld(dh), 1 if pow2 else 0,
+                                        *[_ptr(t) for t in out], _stream(stream, dh))
     _check("fp8_gated_backward_quant", st)
     return out
 
 
-def _grad_arrays(grads):
+def _gradients(grads):
+    """(device pointers, counts, type codes) of a list of gradients, as host arrays."""
+    if not all(g.is_cuda for g in grads):
+        raise ValueError("all tensors must be on the GPU")
+    if not all(g.is_contiguous() for g in grads):
+        raise ValueError("gradients and outputs must be contiguous")
+    return (array("Q", [g.data_ptr() for g in grads]), array("q", [g.numel() for g in grads]),
+            array("i", [_dtype_code(g.dtype) for g in grads]))
+
+
+def _grad_norm(grads, outs, max_norm, norm, workspace, stream):
     n = len(grads)
-    for g in grads:
-        if not g.is_cuda:
-            raise ValueError("all tensors must be on the GPU")
-        if not g.is_contiguous():
-            raise ValueError("gradients and outputs must be contiguous")
-    return ((_c.c_void_p * n)(*[g.data_ptr() for g in grads]), (_c.c_int64 * n)(*[g.numel() for g in grads]),
-            (_c.c_int * n)(*[_dtype_code(g.dtype) for g in grads]))
+    ptrs, counts, dtypes = _gradients(grads)
+    optrs = ptrs
+    if outs is not None and outs is not grads:
+        optrs, ocounts, odtypes = _gradients(outs)
+        if ocounts != counts or odtypes != dtypes:
+            raise ValueError("out must hold one tensor of the same type and length per gradient")
+    dev = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    else:
+        _on_gpu(norm)
+        if norm.dtype != torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must be one fp32 value")
+    L = _lib or lib()
+    ws, nbytes = _workspace(L.fp8fg_grad_norm_workspace(n), workspace, dev, stream)
+    host = [a.buffer_info()[0] for a in (ptrs, optrs, counts, dtypes)]  # (read during the call only)
+    if outs is None:
+        st = L.fp8fg_grad_norm(host[0], host[2], host[3], n, norm.data_ptr(), _ptr(ws), nbytes, _stream(stream, norm))
+        _check("fp8fg_grad_norm", st)
+    else:
+        st = L.fp8fg_clip_grad_norm(host[0], host[1], host[2], host[3], n, max_norm, norm.data_ptr(), _ptr(ws), nbytes,
+                                    _stream(stream, norm))
+        _check("fp8fg_clip_grad_norm", st)
+    return norm
 
 
 def grad_norm(grads, norm=None, workspace=None, stream=None):
     """Global 2-norm over the list ``grads`` (fp32 or bf16, any lengths): an fp32 scalar on the device."""
-    grads = list(grads)
-    ptrs, counts, dtypes = _grad_arrays(grads)
-    dev = grads[0].device if grads else torch.device("cuda")
-    norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
-    ws, nbytes = _workspace(lib().fp8fg_grad_norm_workspace(len(grads)), workspace, dev, stream)
-    st = lib().fp8fg_grad_norm(ptrs, counts, dtypes, len(grads), _ptr(norm), _ptr(ws), nbytes, _stream(stream))
-    _check("fp8fg_grad_norm", st)
-    return norm
+    return _grad_norm(list(grads), None, 0.0, norm, workspace, stream)
 
 
 def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
@@ -315,15 +367,4 @@ def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=
     In place, or into the tensors of ``out`` (same types and lengths).  Returns the
     norm before clipping, an fp32 scalar on the device: no value comes back to the host."""
     grads = list(grads)
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads) or any(o.dtype != g.dtype or o.numel() != g.numel() for o, g in zip(outs, grads)):
-        raise ValueError("out must hold one tensor of the same type and length per gradient")
-    ptrs, counts, dtypes = _grad_arrays(grads)
-    optrs = ptrs if out is None else _grad_arrays(outs)[0]
-    dev = grads[0].device if grads else torch.device("cuda")
-    norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
-    ws, nbytes = _workspace(lib().fp8fg_grad_norm_workspace(len(grads)), workspace, dev, stream)
-    st = lib().fp8fg_clip_grad_norm(ptrs, optrs, counts, dtypes, len(grads), max_norm, _ptr(norm), _ptr(ws), nbytes,
-                                    _stream(stream))
-    _check("fp8fg_clip_grad_norm", st)
-    return norm
+    return _grad_norm(grads, grads if out is None else list(out), max_norm, norm, workspace, stream)

@@ -115,7 +115,7 @@ def test_other_stream_and_graph(gpu):
     torch.cuda.synchronize()
     assert torch.equal(n, ref) and all(torch.equal(a, b) for a, b in zip(outs, refs))
     ws = torch.empty(layer.lib().fp8fg_grad_norm_workspace(3), dtype=torch.uint8, device=gpu)
-    norm = torch.empty(1, device=gpu)
+    norm = torch.empty((), device=gpu)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         layer.clip_grad_norm(grads, 0.5, out=outs, norm=norm, workspace=ws)
