@@ -79,13 +79,20 @@ struct Octet {
       }
     }
   }
+  template <bool NT = false>
   static __device__ __forceinline__ void store(void* g, int part, const float (&f)[8]) {
     u32x4* p = static_cast<u32x4*>(g) + part;
+    auto put = [](const u32x4& v, u32x4* to) {
+      if constexpr (NT)
+        __builtin_nontemporal_store(v, to);
+      else
+        *to = v;
+    };
     if constexpr (BF16) {
-      *p = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+      put(u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])}, p);
     } else {
-      *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
-      *reinterpret_cast<f32x4*>(p + 16) = f32x4{f[4], f[5], f[6], f[7]};
+      put(u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])}, p);
+      put(u32x4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])}, p + 16);
     }
   }
   // The lane's 8 codes into the group's 128-byte code row.

@@ -40,16 +40,21 @@ __device__ __forceinline__ void weight_octet(const void* w, bool w_bf16, int g, 
 }
 
 // ---------------------------------------------------------------- forward
+// Rows of a workgroup whose rows take WPR wavefronts each: four wavefronts at least.
+constexpr int norm_rows(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }
+
 // WPR wavefronts own a row; 16 consecutive lanes own one 128-element group, so
 // a step of the WPR wavefronts covers 512 * WPR elements and CH steps the row.
 template <bool BF16, int WPR, int CH>
-__global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quant_kernel(NormArgs a) {
+__global__ void __launch_bounds__(norm_rows(WPR) * WPR * 64) rmsnorm_quant_kernel(NormArgs a) {
   using O = Octet<BF16>;
-  constexpr int ROWS = WPR >= 4 ? 1 : 4 / WPR;  // rows per workgroup
-  __shared__ float partial[WPR > 1 ? WPR : 1];
-  const int wave = threadIdx.x >> 6;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * ROWS + (ROWS > 1 ? wave / WPR : 0);
-  if (ROWS > 1 && m >= a.M) return;  // whole wavefronts, and no barrier below when ROWS > 1
+  constexpr int ROWS = norm_rows(WPR);
+  __shared__ float partial[ROWS * WPR];
+  const int slot = ROWS == 1 ? 0 : (threadIdx.x >> 6) / WPR;
+  int64_t m = static_cast<int64_t>(blockIdx.x) * ROWS + slot;
+  const bool live = m < a.M;
+  if (WPR == 1 && !live) return;  // whole wavefronts, and no barrier below
+  m = live ? m : a.M - 1;         // else the last row again, not stored
   const int t = threadIdx.x % (WPR * 64);
   const int part = t & 15;
   const int G = static_cast<int>(a.H >> 7);
@@ -79,17 +84,20 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quant_kernel
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(z[c][i], z[c][i], ss);
-      if (a.h) O::store(static_cast<char*>(a.h) + (m * a.H + g * 128) * O::ES, part, z[c]);
+      // (the next reader of h comes after the GEMMs: it need not stay in the caches;
+      // 41.1 -> 39.5 us at 4096 x 7168)
+      if (a.h && live) O::template store<true>(static_cast<char*>(a.h) + (m * a.H + g * 128) * O::ES, part, z[c]);
     }
   }
   ss = sum64(ss);
   if constexpr (WPR > 1) {
-    if ((t & 63) == 0) partial[wave] = ss;
+    if ((t & 63) == 0) partial[threadIdx.x >> 6] = ss;
     __syncthreads();
     ss = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) ss += partial[w];
+    for (int w = 0; w < WPR; ++w) ss += partial[slot * WPR + w];
   }
+  if (!live) return;
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
   if (t == 0 && a.rstd) a.rstd[m] = rstd;
 #pragma unroll
@@ -110,68 +118,93 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256) rmsnorm_quant_kernel
 }
 
 // ---------------------------------------------------------------- backward
-// A workgroup of NW wavefronts holds NW / WPR rows at a time and walks the rows
+// Wavefronts of a workgroup, and the most workgroups of a pass: one per compute
+// unit (twice as many write twice the partials: 46.4 -> 54.5 us at 4096 x 7168).
+constexpr int kGradWaves = 8;
+constexpr int kGradBlocks = 256;
+
+// A workgroup of eight wavefronts holds 8 / WPR rows at a time and walks the rows
 // with a stride of the grid, adding dy * n into registers; at its end its row
 // slots are summed through LDS, in order, into one partial of dw per workgroup,
 // and a second kernel sums the partials, in order: dw is the same on every run.
-template <bool BF16, int WPR, int CH, int NW>
-__global__ void __launch_bounds__(NW * 64) rmsnorm_backward_kernel(NormGradArgs a) {
+template <bool BF16, int WPR, int CH, bool DH>
+__global__ void __launch_bounds__(kGradWaves * 64) rmsnorm_backward_kernel(NormGradArgs a) {
   using O = Octet<BF16>;
-  constexpr int SLOTS = NW / WPR;
-  __shared__ float part_sum[2][NW];
+  constexpr int SLOTS = kGradWaves / WPR;
+  // Long rows leave no registers for a second row and the weights.
+  constexpr bool AHEAD = CH <= (BF16 ? 3 : 2);
+  __shared__ float part_sum[2][kGradWaves];
   extern __shared__ __attribute__((aligned(16))) float dw_sum[];  // [H], when SLOTS > 1 and dw is asked for
   const int wave = threadIdx.x >> 6;
   const int slot = wave / WPR;
   const int t = threadIdx.x % (WPR * 64);
   const int part = t & 15;
   const int G = static_cast<int>(a.H >> 7);
-  float acc[CH][8];
+  // Octets past the row's end read its last group again and count as zero.
+  int col[CH];
+  bool in_row[CH];
+  float acc[CH][8], w[AHEAD ? CH : 1][8];
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
+  for (int c = 0; c < CH; ++c) {
+    const int g = c * (WPR * 4) + (t >> 4);
+    in_row[c] = g < G;
+    col[c] = (g < G ? g : G - 1) * 128;
+    if constexpr (AHEAD) weight_octet<BF16>(a.w, a.w_bf16, col[c] >> 7, part, w[c]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
-
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * SLOTS;
-  int flip = 0;
-  // every slot makes the same number of steps, so that the workgroup's barriers agree
-  for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * SLOTS; m0 < a.M; m0 += stride) {
-    const int64_t m = m0 + slot;
-    const bool live = m < a.M;
-    float d[CH][8], n[CH][8];
-    float dot = 0.0f, rstd = 0.0f;
-    typename O::Raw gr[CH];
-    if (live) {
-      typename O::Raw yr[CH], hr[CH];
-      rstd = a.rstd[m];
-      const char* dy = static_cast<const char*>(a.dy) + m * a.ld_dy * O::ES;
-      const char* h = static_cast<const char*>(a.h) + m * a.ld_h * O::ES;
+  }
+  struct Row {
+    typename O::Raw y[CH], h[CH], dh[CH];
+    float rstd;
+  };
+  // The row's loads, in a straight line (behind a branch the compiler could not
+  // count them and would wait for the next row's before using this one's); rows
+  // past the end read the last one.
+  auto load = [&](Row& r, int64_t m) {
+    m = m < a.M ? m : a.M - 1;
+    const char* dy = static_cast<const char*>(a.dy) + m * a.ld_dy * O::ES;
+    const char* h = static_cast<const char*>(a.h) + m * a.ld_h * O::ES;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      r.y[c] = O::load(dy + static_cast<int64_t>(col[c]) * O::ES, part);
+      r.h[c] = O::load(h + static_cast<int64_t>(col[c]) * O::ES, part);
+    }
+    if constexpr (DH) {
       const char* dh = static_cast<const char*>(a.dh) + m * a.ld_dh * O::ES;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int g = c * (WPR * 4) + (t >> 4);
-        if (g < G) {
-          yr[c] = O::load(dy + static_cast<int64_t>(g) * 128 * O::ES, part);
-          hr[c] = O::load(h + static_cast<int64_t>(g) * 128 * O::ES, part);
-          if (a.dh) gr[c] = O::load(dh + static_cast<int64_t>(g) * 128 * O::ES, part);
-        }
+      for (int c = 0; c < CH; ++c) r.dh[c] = O::load(dh + static_cast<int64_t>(col[c]) * O::ES, part);
+    }
+    r.rstd = a.rstd[m];
+  };
+  int flip = 0;
+  auto process = [&](Row& r, int64_t m) __attribute__((always_inline)) {
+    const bool live = m < a.M;
+    // dy and n of octet c, and its weights
+    auto form = [&](int c, float (&y)[8], float (&n)[8], float (&wc)[8]) __attribute__((always_inline)) {
+      O::widen(r.y[c], y);
+      O::widen(r.h[c], n);
+      if constexpr (!AHEAD) {
+        int g = col[c] >> 7;
+        asm volatile("" : "+v"(g));  // else the compiler keeps every weight in registers over the rows
+        weight_octet<BF16>(a.w, a.w_bf16, g, part, wc);
       }
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int g = c * (WPR * 4) + (t >> 4);
-        if (g < G) {
-          float w[8];
-          weight_octet<BF16>(a.w, a.w_bf16, g, part, w);
-          O::widen(yr[c], d[c]);
-          O::widen(hr[c], n[c]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            n[c][i] *= rstd;
-            acc[c][i] = fmaf(d[c][i], n[c][i], acc[c][i]);
-            d[c][i] *= w[i];
-            dot = fmaf(d[c][i], n[c][i], dot);
-          }
-        }
+      for (int i = 0; i < 8; ++i) {
+        n[i] *= r.rstd;
+        if constexpr (AHEAD) wc[i] = w[c][i];
       }
+    };
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float y[8], n[8], wc[8];
+      form(c, y, n, wc);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (live && in_row[c]) acc[c][i] = fmaf(y[i], n[i], acc[c][i]);
+        if (in_row[c]) dot = fmaf(y[i] * wc[i], n[i], dot);
+      }
+      if constexpr (!AHEAD) __builtin_amdgcn_sched_barrier(0);  // octet by octet: fewer live registers
     }
     dot = sum64(dot);
     if constexpr (WPR > 1) {
@@ -180,25 +213,54 @@ __global__ void __launch_bounds__(NW * 64) rmsnorm_backward_kernel(NormGradArgs 
       __syncthreads();
       dot = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) dot += part_sum[flip][slot * WPR + w];
+      for (int v = 0; v < WPR; ++v) dot += part_sum[flip][slot * WPR + v];
       flip ^= 1;
     }
+    const float c0 = dot / static_cast<float>(a.H);
     if (live) {
-      const float c0 = dot / static_cast<float>(a.H);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int g = c * (WPR * 4) + (t >> 4);
-        if (g < G) {
-          float o[8];
-          if (a.dh) O::widen(gr[c], o);
+        if (in_row[c]) {
+          float y[8], n[8], wc[8], o[8];
+          if constexpr (!AHEAD) {
+            // formed again from the loaded values, which this hides from the
+            // compiler: kept in fp32 they would spill
+#pragma unroll
+            for (int k = 0; k < (BF16 ? 1 : 2); ++k) asm volatile("" : "+v"(r.y[c].v[k]), "+v"(r.h[c].v[k]));
+          }
+          form(c, y, n, wc);
+          if constexpr (DH) O::widen(r.dh[c], o);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float v = rstd * fmaf(-n[c][i], c0, d[c][i]);
-            o[i] = a.dh ? v + o[i] : v;
+            const float v = r.rstd * fmaf(-n[i], c0, y[i] * wc[i]);
+            o[i] = DH ? v + o[i] : v;
           }
-          O::store(static_cast<char*>(a.dx) + (m * a.H + g * 128) * O::ES, part, o);
+          O::store(static_cast<char*>(a.dx) + (m * a.H + col[c]) * O::ES, part, o);
         }
+        if constexpr (!AHEAD) __builtin_amdgcn_sched_barrier(0);
       }
+    }
+  };
+  // Every slot makes the same number of steps, so that the workgroup's barriers
+  // agree.  The next row loads while this one is reduced and written (54.6 -> 46.4
+  // us at 4096 x 7168).
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * SLOTS;
+  int64_t m0 = static_cast<int64_t>(blockIdx.x) * SLOTS;
+  if constexpr (AHEAD) {
+    Row r0, r1;
+    load(r0, m0 + slot);
+    for (; m0 < a.M; m0 += 2 * stride) {
+      load(r1, m0 + stride + slot);
+      process(r0, m0 + slot);
+      if (m0 + stride >= a.M) break;
+      load(r0, m0 + 2 * stride + slot);
+      process(r1, m0 + stride + slot);
+    }
+  } else {
+    for (; m0 < a.M; m0 += stride) {
+      Row r;
+      load(r, m0 + slot);
+      process(r, m0 + slot);
     }
   }
   if (!a.partial) return;
@@ -227,15 +289,23 @@ __global__ void __launch_bounds__(NW * 64) rmsnorm_backward_kernel(NormGradArgs 
   }
 }
 
-// dw[j] = sum of the P partials of column j.  A workgroup takes 32 columns: 8
+// dw[j] = sum of the P <= kGradBlocks partials of column j.  A workgroup takes 32 columns: 8
 // lanes of four columns by 32 strided row sums, added pairwise through LDS.
 __global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* __restrict__ partial, int P, int64_t H,
                                                          float* __restrict__ dw) {
   __shared__ __attribute__((aligned(16))) f32x4 sums[32][8];
   const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + c * 4;
-  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int p = r; p < P; p += 32) v += *reinterpret_cast<const f32x4*>(partial + p * H + j);
+  f32x4 part[kGradBlocks / 32];  // loaded together: one latency instead of eight
+#pragma unroll
+  for (int i = 0; i < kGradBlocks / 32; ++i) {
+    const int p = r + 32 * i;
+    part[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (p < P) part[i] = *reinterpret_cast<const f32x4*>(partial + p * H + j);
+  }
+  f32x4 v = part[0];
+#pragma unroll
+  for (int i = 1; i < kGradBlocks / 32; ++i) v += part[i];
   sums[r][c] = v;
 #pragma unroll
   for (int n = 16; n >= 1; n >>= 1) {
@@ -245,33 +315,46 @@ __global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* __restrict
   if (r == 0) *reinterpret_cast<f32x4*>(dw + j) = sums[0][c];
 }
 
-// Wavefronts per row and steps per row for H: the fewest registers per lane that
-// still hold a row (CH octets of 8 elements).
+// Wavefronts per row and octets per lane for rows of H elements.  More wavefronts
+// shorten a row's latency, fewer leave less of them idle; at 7168 (4096 rows, bf16)
+// 8 x 2 octets take 38.8 us forward and 46.4 backward, 4 x 4 39.9 and 57.3, 16 x 1
+// 43.7 and 46.7, and one row alone takes 3.5, 4.7 and 3.1 us forward.  The backward
+// pass, which keeps dw in registers as well, stays at eight wavefronts, with 256
+// registers a lane (18432, 4096 rows: 16 x 3 spilled, 363 us).
+#define FP8FG_SHAPE(WPR, CH) f(std::integral_constant<int, WPR>{}, std::integral_constant<int, CH>{})
 template <typename F>
-hipError_t with_shape(int64_t H, F&& f) {
-  using std::integral_constant;
-#define FP8FG_SHAPE(WPR, CH) f(integral_constant<int, WPR>{}, integral_constant<int, CH>{})
+hipError_t with_short_shape(int64_t H, F&& f) {
   if (H <= 512) return FP8FG_SHAPE(1, 1);
-  if (H <= 1024) return FP8FG_SHAPE(1, 2);
+  if (H <= 1024) return FP8FG_SHAPE(2, 1);
   if (H <= 2048) return FP8FG_SHAPE(4, 1);
-  if (H <= 4096) return FP8FG_SHAPE(4, 2);
-  if (H <= 8192) return FP8FG_SHAPE(4, 4);
-  if (H <= 16384) return FP8FG_SHAPE(16, 2);
-  return FP8FG_SHAPE(16, 4);  // H <= 32768
-#undef FP8FG_SHAPE
+  if (H <= 4096) return FP8FG_SHAPE(8, 1);
+  return FP8FG_SHAPE(8, 2);  // H <= 8192
 }
-
-// Wavefronts of a backward workgroup, and the most workgroups of one pass.
-constexpr int grad_waves(int wpr) { return wpr > 8 ? wpr : 8; }
-constexpr int kGradBlocks = 512;
+template <typename F>
+hipError_t with_forward_shape(int64_t H, F&& f) {
+  if (H <= 8192) return with_short_shape(H, f);
+  if (H <= 16384) return FP8FG_SHAPE(16, 2);
+  if (H <= 24576) return FP8FG_SHAPE(16, 3);
+  return FP8FG_SHAPE(16, 4);  // kNormMaxH
+}
+template <typename F>
+hipError_t with_backward_shape(int64_t H, F&& f) {
+  if (H <= 8192) return with_short_shape(H, f);
+  if (H <= 12288) return FP8FG_SHAPE(8, 3);
+  if (H <= 16384) return FP8FG_SHAPE(8, 4);
+  if (H <= 20480) return FP8FG_SHAPE(8, 5);
+  if (H <= 24576) return FP8FG_SHAPE(8, 6);
+  return FP8FG_SHAPE(8, 8);  // kNormMaxH
+}
+#undef FP8FG_SHAPE
 
 }  // namespace
 
 hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t s) {
-  return with_shape(a.H, [&](auto wpr, auto ch) {
+  return with_forward_shape(a.H, [&](auto wpr, auto ch) {
     constexpr int WPR = decltype(wpr)::value, CH = decltype(ch)::value;
-    constexpr int ROWS = WPR >= 4 ? 1 : 4 / WPR;
-    const dim3 grid(static_cast<unsigned>((a.M + ROWS - 1) / ROWS)), block(WPR > 4 ? WPR * 64 : 256);
+    constexpr int ROWS = norm_rows(WPR);
+    const dim3 grid(static_cast<unsigned>((a.M + ROWS - 1) / ROWS)), block(ROWS * WPR * 64);
     if (a.bf16)
       hipLaunchKernelGGL((rmsnorm_quant_kernel<true, WPR, CH>), grid, block, 0, s, a);
     else
@@ -282,8 +365,8 @@ hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t s) {
 
 int64_t rmsnorm_backward_partials(int64_t M, int64_t H) {
   int64_t p = 0;
-  (void)with_shape(H, [&](auto wpr, auto) {
-    constexpr int WPR = decltype(wpr)::value, SLOTS = grad_waves(WPR) / WPR;
+  (void)with_backward_shape(H, [&](auto wpr, auto) {
+    constexpr int WPR = decltype(wpr)::value, SLOTS = kGradWaves / WPR;
     p = (M + SLOTS - 1) / SLOTS;
     return hipSuccess;
   });
@@ -294,15 +377,16 @@ hipError_t launch_rmsnorm_backward(const NormGradArgs& a, float* dw, hipStream_t
   const int64_t P = rmsnorm_backward_partials(a.M, a.H);
   hipError_t e = hipSuccess;
   if (P > 0) {
-    e = with_shape(a.H, [&](auto wpr, auto ch) {
+    e = with_backward_shape(a.H, [&](auto wpr, auto ch) {
       constexpr int WPR = decltype(wpr)::value, CH = decltype(ch)::value;
-      constexpr int NW = grad_waves(WPR);
-      const size_t lds = NW > WPR && a.partial ? a.H * sizeof(float) : 0;
-      const dim3 grid(static_cast<unsigned>(P)), block(NW * 64);
+      const size_t lds = WPR < kGradWaves && a.partial ? a.H * sizeof(float) : 0;
+      const dim3 grid(static_cast<unsigned>(P)), block(kGradWaves * 64);
+      auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, s, a); };
       if (a.bf16)
-        hipLaunchKernelGGL((rmsnorm_backward_kernel<true, WPR, CH, NW>), grid, block, lds, s, a);
+        a.dh ? go(rmsnorm_backward_kernel<true, WPR, CH, true>) : go(rmsnorm_backward_kernel<true, WPR, CH, false>);
       else
-        hipLaunchKernelGGL((rmsnorm_backward_kernel<false, WPR, CH, NW>), grid, block, lds, s, a);
+        a.dh ? go(rmsnorm_backward_kernel<false, WPR, CH, true>)
+             : go(rmsnorm_backward_kernel<false, WPR, CH, false>);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
