@@ -6,6 +6,7 @@
 // gradient dW = dGU^T X); h leaves transposed for the down projection's weight
 // gradient dW2 = dY^T h.  One pass: dh, g and u are read once, 11 bytes move per
 // (token, column) in bf16, and HBM is the bound.
+#include "activation.h"
 #include "launch.h"
 #include "lanes.h"
 
@@ -25,7 +26,7 @@ struct Grads {
     O::widen(ru, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float p = 1.0f / (1.0f + expf(-g[i]));
+      const float p = sigmoid(g[i]);
       const float gp = g[i] * p;
       h[i] = gp * u[i];
       const float dg = d[i] * u[i] * p * fmaf(g[i], 1.0f - p, 1.0f);
@@ -62,9 +63,8 @@ __global__ void __launch_bounds__(256) gated_backward_rows_kernel(GatedGradArgs 
 // A 512-thread workgroup owns 128 tokens x 128 columns of dh, g and u.  Thread
 // (rg, part) holds rows 4 rg .. 4 rg + 3 and the 8 columns of lane `part`, so its
 // four tokens of a column are one dword of the transposed codes.  Column maxima
-// go over the wavefront's four row groups by lane exchange and over the eight
-// wavefronts through LDS; the transposed codes are staged there as well and
-// leave as whole 128-byte runs.  LDS rows are 36 dwords apart and their 16-byte
+// meet in LDS; the transposed codes are staged there as well and leave as whole
+// 128-byte runs.  LDS rows are 36 dwords apart and their 16-byte
 // pieces permuted by the column, so the 64 lanes of a store hit 64 banks.
 constexpr int kPitch = 36;
 
@@ -76,8 +76,10 @@ __device__ __forceinline__ int piece_key(int c) {
 template <bool BF16>
 __global__ void __launch_bounds__(512) gated_backward_tile_kernel(GatedGradArgs a) {
   using O = Octet<BF16>;
-  __shared__ __attribute__((aligned(16))) uint32_t tile[3][128 * kPitch];
-  __shared__ float wave_max[3][8][128];
+  __shared__ __attribute__((aligned(16))) union {
+    uint32_t tile[3][128 * kPitch];
+    float max[3][32][128];  // before the codes
+  } lds;
   __shared__ float inverse[3][128];
   const int tid = threadIdx.x;
   const int part = tid & 15, rg = tid >> 4;
@@ -89,54 +91,56 @@ __global__ void __launch_bounds__(512) gated_backward_tile_kernel(GatedGradArgs 
   const int64_t tg = b % TG, c0 = b / TG * 128;
   Grads<BF16> v[4];
   {
+    // Every load goes out first; then row by row, so that a row's loaded registers
+    // are free before the next row's results need theirs.
     typename O::Raw rd[4], rgt[4], ru[4];
+    const char* dh = static_cast<const char*>(a.dh) + ((tg * 128 + 4 * rg) * a.ld_dh + c0) * O::ES;
+    const char* gu = static_cast<const char*>(a.gu) + ((tg * 128 + 4 * rg) * 2 * a.I + c0) * O::ES;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t m = tg * 128 + 4 * rg + i;
-      const char* gu = static_cast<const char*>(a.gu) + (m * 2 * a.I + c0) * O::ES;
-      rd[i] = O::load(static_cast<const char*>(a.dh) + (m * a.ld_dh + c0) * O::ES, part);
-      rgt[i] = O::load(gu, part);
-      ru[i] = O::load(gu + a.I * O::ES, part);
+      rd[i] = O::load(dh + i * a.ld_dh * O::ES, part);
+      rgt[i] = O::load(gu + i * 2 * a.I * O::ES, part);
+      ru[i] = O::load(gu + (2 * i + 1) * a.I * O::ES, part);
     }
+    uint8_t* q = a.q + (tg * 128 + 4 * rg) * 2 * a.I + c0;
+    float* s_out = a.s + (tg * 128 + 4 * rg) * 2 * G + (c0 >> 7);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i].form(rd[i], rgt[i], ru[i]);
+    for (int i = 0; i < 4; ++i) {
+      v[i].form(rd[i], rgt[i], ru[i]);
+      if (a.q) {
+        float s, inv;
+        group_scale(a.pow2, group_amax(v[i].g), s, inv);
+        O::store_codes(q + 2 * i * a.I, part, v[i].g, inv);
+        if (part == 0) s_out[2 * i * G] = s;
+        group_scale(a.pow2, group_amax(v[i].u), s, inv);
+        O::store_codes(q + (2 * i + 1) * a.I, part, v[i].u, inv);
+        if (part == 0) s_out[(2 * i + 1) * G] = s;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  if (a.q) {
+  // column maxima: the thread's four rows, then the workgroup's 32 row groups
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = tg * 128 + 4 * rg + i;
-      float s, inv;
-      group_scale(a.pow2, group_amax(v[i].g), s, inv);
-      O::store_codes(a.q + m * 2 * a.I + c0, part, v[i].g, inv);
-      if (part == 0) a.s[m * 2 * G + (c0 >> 7)] = s;
-      group_scale(a.pow2, group_amax(v[i].u), s, inv);
-      O::store_codes(a.q + m * 2 * a.I + a.I + c0, part, v[i].u, inv);
-      if (part == 0) a.s[m * 2 * G + G + (c0 >> 7)] = s;
-    }
-  }
-  // column maxima: the thread's rows, the wavefront's, the workgroup's
+  for (int k = 0; k < 3; ++k) {
+    float mx[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float mx[3] = {0.0f, 0.0f, 0.0f};
+    for (int e = 0; e < 8; ++e) {
+      mx[e] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      mx[0] = fmaxf(mx[0], fabsf(v[i].g[e]));
-      mx[1] = fmaxf(mx[1], fabsf(v[i].u[e]));
-      mx[2] = fmaxf(mx[2], fabsf(v[i].h[e]));
+      for (int i = 0; i < 4; ++i)
+        mx[e] = fmaxf(mx[e], fabsf(k == 0 ? v[i].g[e] : k == 1 ? v[i].u[e] : v[i].h[e]));
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      mx[k] = fmaxf(mx[k], __shfl_xor(mx[k], 16));
-      mx[k] = fmaxf(mx[k], __shfl_xor(mx[k], 32));
-      if ((tid & 63) < 16) wave_max[k][tid >> 6][O::col(part, e)] = mx[k];
-    }
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<f32x4*>(&lds.max[k][rg][O::col(part, 4 * h)]) =
+          f32x4{mx[4 * h], mx[4 * h + 1], mx[4 * h + 2], mx[4 * h + 3]};
   }
   __syncthreads();
   if (tid < 384) {
     const int k = tid >> 7, c = tid & 127;
     float mx = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) mx = fmaxf(mx, wave_max[k][w][c]);
+    for (int r = 0; r < 32; ++r) mx = fmaxf(mx, lds.max[k][r][c]);
     float s, inv;
     group_scale(a.pow2, mx, s, inv);
     inverse[k][c] = inv;
@@ -149,9 +153,9 @@ __global__ void __launch_bounds__(512) gated_backward_tile_kernel(GatedGradArgs 
     const int c = O::col(part, e);
     const int at = c * kPitch + (rg ^ (piece_key<BF16>(c) << 2));
     const float ig = inverse[0][c], iu = inverse[1][c], ih = inverse[2][c];
-    tile[0][at] = cvt4(v[0].g[e] * ig, v[1].g[e] * ig, v[2].g[e] * ig, v[3].g[e] * ig);
-    tile[1][at] = cvt4(v[0].u[e] * iu, v[1].u[e] * iu, v[2].u[e] * iu, v[3].u[e] * iu);
-    tile[2][at] = cvt4(v[0].h[e] * ih, v[1].h[e] * ih, v[2].h[e] * ih, v[3].h[e] * ih);
+    lds.tile[0][at] = cvt4(v[0].g[e] * ig, v[1].g[e] * ig, v[2].g[e] * ig, v[3].g[e] * ig);
+    lds.tile[1][at] = cvt4(v[0].u[e] * iu, v[1].u[e] * iu, v[2].u[e] * iu, v[3].u[e] * iu);
+    lds.tile[2][at] = cvt4(v[0].h[e] * ih, v[1].h[e] * ih, v[2].h[e] * ih, v[3].h[e] * ih);
   }
   __syncthreads();
 #pragma unroll
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(512) gated_backward_tile_kernel(GatedGradArgs 
     for (int j = 0; j < 2; ++j) {
       const int c = (tid + 512 * j) >> 3, ch = tid & 7;
       *reinterpret_cast<u32x4*>(out + ((k == 1 ? a.I : 0) + c0 + c) * a.M + tg * 128 + ch * 16) =
-          *reinterpret_cast<const u32x4*>(&tile[k][c * kPitch + 4 * (ch ^ piece_key<BF16>(c))]);
+          *reinterpret_cast<const u32x4*>(&lds.tile[k][c * kPitch + 4 * (ch ^ piece_key<BF16>(c))]);
     }
   }
 }
