@@ -214,7 +214,7 @@ int fp8_gated_backward_quant(const void* dh, const void* gu, int dtype, int64_t 
   if (!q && !q_t && !q_ht) return FP8FG_ERR_INVALID_ARG;
   if (I % 128 != 0 || ((q_t || q_ht) && M % 128 != 0)) return FP8FG_ERR_UNSUPPORTED;
   // launch grids: one workgroup per 128 x 128 tile, or per 16 groups of a row
-  if (M > kInt32Max || I > kInt32Max || M * (I / 128) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;
+  if (M > kInt32Max || I > kInt32Max || M * (I / 128) > kInt32Max - 8) return FP8FG_ERR_UNSUPPORTED;
   const int c = check_rows(dh, dtype, I, ld_dh);
   if (c != FP8FG_OK) return c;
   if (!gu) return FP8FG_ERR_INVALID_ARG;
