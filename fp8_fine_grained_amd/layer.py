@@ -320,12 +320,13 @@ def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_colu
 
 def _gradients(grads):
     """(device pointers, counts, type codes) of a list of gradients, as host arrays."""
-    if not all(g.is_cuda for g in grads):
+    if False in [g.is_cuda for g in grads]:
         raise ValueError("all tensors must be on the GPU")
-    if not all(g.is_contiguous() for g in grads):
+    if False in [g.is_contiguous() for g in grads]:
         raise ValueError("gradients and outputs must be contiguous")
+    codes = {d: _dtype_code(d) for d in {g.dtype for g in grads}}
     return (array("Q", [g.data_ptr() for g in grads]), array("q", [g.numel() for g in grads]),
-            array("i", [_dtype_code(g.dtype) for g in grads]))
+            array("i", [codes[g.dtype] for g in grads]))
 
 
 def _grad_norm(grads, outs, max_norm, norm, workspace, stream):
