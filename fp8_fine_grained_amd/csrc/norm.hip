@@ -45,7 +45,9 @@ constexpr int norm_rows(int wpr) { return wpr >= 4 ? 1 : 4 / wpr; }
 
 // WPR wavefronts own a row; 16 consecutive lanes own one 128-element group, so
 // a step of the WPR wavefronts covers 512 * WPR elements and CH steps the row.
-template <bool BF16, int WPR, int CH>
+// (Fewer workgroups, each walking over rows with the next row's loads ahead, as the
+// backward pass does, were slower: 44 us and more against 37.5 at 4096 x 7168.)
+template <bool BF16, int WPR, int CH, bool RES>
 __global__ void __launch_bounds__(norm_rows(WPR) * WPR * 64) rmsnorm_quant_kernel(NormArgs a) {
   using O = Octet<BF16>;
   constexpr int ROWS = norm_rows(WPR);
@@ -53,41 +55,38 @@ __global__ void __launch_bounds__(norm_rows(WPR) * WPR * 64) rmsnorm_quant_kerne
   const int slot = ROWS == 1 ? 0 : (threadIdx.x >> 6) / WPR;
   int64_t m = static_cast<int64_t>(blockIdx.x) * ROWS + slot;
   const bool live = m < a.M;
-  if (WPR == 1 && !live) return;  // whole wavefronts, and no barrier below
-  m = live ? m : a.M - 1;         // else the last row again, not stored
+  m = live ? m : a.M - 1;  // past the end: the last row again, not stored
   const int t = threadIdx.x % (WPR * 64);
   const int part = t & 15;
   const int G = static_cast<int>(a.H >> 7);
+  typename O::Raw xr[CH], rr[CH];
   const char* x = static_cast<const char*>(a.x) + m * a.ld_x * O::ES;
   const char* r = static_cast<const char*>(a.r) + m * a.ld_r * O::ES;
-  float z[CH][8];
-  typename O::Raw xr[CH], rr[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int g = c * (WPR * 4) + (t >> 4);
-    if (g < G) {
-      xr[c] = O::load(x + static_cast<int64_t>(g) * 128 * O::ES, part);
-      if (a.r) rr[c] = O::load(r + static_cast<int64_t>(g) * 128 * O::ES, part);
-    }
+    if (g >= G) continue;
+    xr[c] = O::load(x + static_cast<int64_t>(g) * 128 * O::ES, part);
+    if constexpr (RES) rr[c] = O::load(r + static_cast<int64_t>(g) * 128 * O::ES, part);
   }
+  float z[CH][8];
   float ss = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int g = c * (WPR * 4) + (t >> 4);
-    if (g < G) {
-      O::widen(xr[c], z[c]);
-      if (a.r) {
-        float v[8];
-        O::widen(rr[c], v);
+    if (g >= G) continue;
+    O::widen(xr[c], z[c]);
+    if constexpr (RES) {
+      float v[8];
+      O::widen(rr[c], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[c][i] += v[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(z[c][i], z[c][i], ss);
-      // (the next reader of h comes after the GEMMs: it need not stay in the caches;
-      // 41.1 -> 39.5 us at 4096 x 7168)
-      if (a.h && live) O::template store<true>(static_cast<char*>(a.h) + (m * a.H + g * 128) * O::ES, part, z[c]);
+      for (int i = 0; i < 8; ++i) z[c][i] += v[i];
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(z[c][i], z[c][i], ss);
+    // (the next reader of h comes after the GEMMs: it need not stay in the caches;
+    // 41.1 -> 39.5 us at 4096 x 7168)
+    if (a.h && live) O::template store<true>(static_cast<char*>(a.h) + (m * a.H + g * 128) * O::ES, part, z[c]);
   }
   ss = sum64(ss);
   if constexpr (WPR > 1) {
@@ -355,10 +354,11 @@ hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t s) {
     constexpr int WPR = decltype(wpr)::value, CH = decltype(ch)::value;
     constexpr int ROWS = norm_rows(WPR);
     const dim3 grid(static_cast<unsigned>((a.M + ROWS - 1) / ROWS)), block(ROWS * WPR * 64);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
     if (a.bf16)
-      hipLaunchKernelGGL((rmsnorm_quant_kernel<true, WPR, CH>), grid, block, 0, s, a);
+      a.r ? go(rmsnorm_quant_kernel<true, WPR, CH, true>) : go(rmsnorm_quant_kernel<true, WPR, CH, false>);
     else
-      hipLaunchKernelGGL((rmsnorm_quant_kernel<false, WPR, CH>), grid, block, 0, s, a);
+      a.r ? go(rmsnorm_quant_kernel<false, WPR, CH, true>) : go(rmsnorm_quant_kernel<false, WPR, CH, false>);
     return hipGetLastError();
   });
 }
