@@ -106,6 +106,23 @@ def _like(what, dtype, shape, *ts):
             raise ValueError(f"{what} must be {dtype} {list(shape)}")
 
 
+def _given(what, dtype, shape, *ts):
+    """Checks of tensors that a kernel takes contiguous: a caller's outputs, saved values."""
+    for t in ts:
+        if t is not None:
+            if t.dtype != dtype or t.shape != shape:
+                raise ValueError(f"{what} must be {dtype} {list(shape)}")
+            if not t.is_cuda:
+                raise ValueError("all tensors must be on the GPU")
+            if not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous")
+
+
+def _weight(w, H):
+    if w.shape != (H,) or not w.is_contiguous():
+        raise ValueError("weight must be contiguous [H]")
+
+
 def fp8_add_rmsnorm_quant_1x128(x, weight, residual=None, eps=1e-6, pow2=False, h=None, y=None, q=None, scales=None,
                                 rstd=None, stream=None):
     """Residual addition, RMS norm and 1x128 quantisation of ``x`` [M, H] in one pass.
@@ -114,25 +131,28 @@ def fp8_add_rmsnorm_quant_1x128(x, weight, residual=None, eps=1e-6, pow2=False, 
     Pass ``y`` (of x's type) to also have the normed rows in high precision.
     Returns ``(h, q uint8 [M, H], scales fp32 [M, H/128], rstd fp32 [M])``;
     ``h`` is x + residual rounded to x's type, and x itself without a residual."""
-    _on_gpu(x, weight, residual, h, y, q, scales, rstd)
+    _on_gpu(x, weight, residual)
     _rows(x, residual)
     M, H = x.shape
-    dt, dev = x.dtype, x.device
-    _like("residual, h and y", dt, (M, H), residual, h, y)
-    _like("q", torch.uint8, (M, H), q)
-    _like("scales", torch.float32, (M, H // 128), scales)
-    _like("rstd", torch.float32, (M,), rstd)
-    _contig(*[t for t in (weight, h, y, q, scales, rstd) if t is not None])
-    if weight.shape != (H,):
-        raise ValueError("weight must be contiguous [H]")
+    dt = x.dtype
+    _like("residual", dt, (M, H), residual)
+    _weight(weight, H)
+    if h is not None or y is not None:
+        _given("h and y", dt, (M, H), h, y)
     if residual is not None and h is None:
-        h = torch.empty((M, H), dtype=dt, device=dev)
+        h = x.new_empty((M, H))
     if q is None:
-        q = torch.empty((M, H), dtype=torch.uint8, device=dev)
+        q = x.new_empty((M, H), dtype=torch.uint8)
+    else:
+        _given("q", torch.uint8, (M, H), q)
     if scales is None:
-        scales = torch.empty((M, H // 128), dtype=torch.float32, device=dev)
+        scales = x.new_empty((M, H // 128), dtype=torch.float32)
+    else:
+        _given("scales", torch.float32, (M, H // 128), scales)
     if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        rstd = x.new_empty(M, dtype=torch.float32)
+    else:
+        _given("rstd", torch.float32, (M,), rstd)
     st = (_lib or lib()).fp8_add_rmsnorm_quant_1x128(
         x.data_ptr(), _ptr(residual), _dtype_code(dt), M, H, _ld(x), _ld(residual), weight.data_ptr(),
         _dtype_code(weight.dtype), eps, 1 if pow2 else 0, _ptr(h), _ptr(y), q.data_ptr(), scales.data_ptr(),
@@ -146,19 +166,20 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
 
     ``h`` and ``rstd`` as the forward call returned them; ``dh`` is the gradient
     that arrives along the residual stream.  ``need_dw=False``: dw is None."""
-    _on_gpu(dy, h, rstd, weight, dh, dx, dw)
+    _on_gpu(dy, h, rstd, weight, dh)
     _rows(dy, h, dh)
     M, H = dy.shape
-    _like("h, dh and dx", dy.dtype, (M, H), h, dh, dx)
-    _like("rstd", torch.float32, (M,), rstd)
-    _like("dw", torch.float32, (H,), dw)
-    _contig(*[t for t in (rstd, weight, dx, dw) if t is not None])
-    if weight.shape != (H,):
-        raise ValueError("weight must be contiguous [H]")
+    _like("h and dh", dy.dtype, (M, H), h, dh)
+    _given("rstd", torch.float32, (M,), rstd)
+    _weight(weight, H)
     if dx is None:
-        dx = torch.empty((M, H), dtype=dy.dtype, device=dy.device)
-    if dw is None and need_dw:
-        dw = torch.empty(H, dtype=torch.float32, device=dy.device)
+        dx = dy.new_empty((M, H))
+    else:
+        _given("dx", dy.dtype, (M, H), dx)
+    if dw is not None:
+        _given("dw", torch.float32, (H,), dw)
+    elif need_dw:
+        dw = dy.new_empty(H, dtype=torch.float32)
     L = _lib or lib()
     ws, nbytes = None, 0
     if dw is not None:
@@ -172,42 +193,36 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
 
 def _gated_operands(a, sa, w, sw, rows):
     """Shapes of a gated product: (K, I) after checking operands against each other."""
-    _on_gpu(a, sa, w, sw)
-    _contig(a, sa, w, sw)
     K, I2 = a.shape[1], w.shape[-2]
     lead = w.shape[:-2]
-    _like("a", torch.uint8, (rows, K), a)
-    _like("sa", torch.float32, (rows, K // 128), sa)
-    _like("w", torch.uint8, (*lead, I2, K), w)
+    _given("a", torch.uint8, (rows, K), a)
+    _given("sa", torch.float32, (rows, K // 128), sa)
+    _given("w", torch.uint8, (*lead, I2, K), w)
     if I2 % 256 != 0 or K % 128 != 0:  # (the library's own refusal, before a shape check could hide it)
         raise binding.Fp8fgError("gated product", binding.ERR_UNSUPPORTED)
-    _like("sw", torch.float32, (*lead, I2 // 128, K // 128), sw)
+    _given("sw", torch.float32, (*lead, I2 // 128, K // 128), sw)
     return K, I2 // 2
 
 
-def _gated_outputs(rows, inner, dtype, dev, h, gu, save):
+def _gated_outputs(rows, inner, dtype, a, h, gu, save):
+    """h (or its codes, dtype uint8) and gu, allocated beside ``a`` where they are not given."""
     if h is None:
-        h = torch.empty((rows, inner), dtype=dtype, device=dev)
+        h = a.new_empty((rows, inner), dtype=dtype)
     else:
-        _on_gpu(h)
-        _like("h", h.dtype if dtype != torch.uint8 else dtype, (rows, inner), h)
-        _contig(h)
-    gu_dtype = torch.bfloat16 if dtype == torch.uint8 else h.dtype
-    if gu is not None:
-        _on_gpu(gu)
-        _like("gu", gu_dtype, (rows, 2 * inner), gu)
-        _contig(gu)
-    elif save:
-        gu = torch.empty((rows, 2 * inner), dtype=gu_dtype, device=dev)
+        _given("h", h.dtype if dtype != torch.uint8 else dtype, (rows, inner), h)
+    if gu is not None or save:
+        gu_dtype = torch.bfloat16 if dtype == torch.uint8 else h.dtype
+        if gu is None:
+            gu = a.new_empty((rows, 2 * inner), dtype=gu_dtype)
+        else:
+            _given("gu", gu_dtype, (rows, 2 * inner), gu)
     return h, gu
 
 
-def _scales_out(rows, inner, dev, scales):
+def _scales_out(rows, inner, a, scales):
     if scales is None:
-        return torch.empty((rows, inner // 128), dtype=torch.float32, device=dev)
-    _on_gpu(scales)
-    _like("scales", torch.float32, (rows, inner // 128), scales)
-    _contig(scales)
+        return a.new_empty((rows, inner // 128), dtype=torch.float32)
+    _given("scales", torch.float32, (rows, inner // 128), scales)
     return scales
 
 
@@ -220,7 +235,7 @@ def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=N
     g and u [M, 2I] for the backward pass: returns ``(h, gu)``, else ``h``."""
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw, M)
-    h, gu = _gated_outputs(M, inner, out_dtype, a.device, h, gu, save)
+    h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
     st = (_lib or lib()).fp8_block_gated_gemm(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h),
                                     _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream, a))
     _check("fp8_block_gated_gemm", st)
@@ -233,8 +248,8 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
     and the bf16 ``gu`` [M, 2I] as a third with ``save=True``."""
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw, M)
-    q, gu = _gated_outputs(M, inner, torch.uint8, a.device, q, gu, save)
-    scales = _scales_out(M, inner, a.device, scales)
+    q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
+    scales = _scales_out(M, inner, a, scales)
     mode = _accum_code(accum, torch.bfloat16)
     ws, nbytes = _workspace((_lib or lib()).fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device, stream)
     st = (_lib or lib()).fp8_block_gated_gemm_quant(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), mode, 1 if pow2 else 0, _ptr(q),
@@ -263,7 +278,7 @@ def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=No
     of ``a`` itself.  Returns ``h`` [M_total, I] (and ``gu``) in routed-row order."""
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
-    h, gu = _gated_outputs(M, inner, out_dtype, a.device, h, gu, save)
+    h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
     st = (_lib or lib()).fp8_block_grouped_gated_gemm(
         _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw),
         _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream, a))
@@ -276,8 +291,8 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
     """The same with h leaving 1x128-quantised: ``(q, scales)``, and ``gu`` with ``save=True``."""
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
-    q, gu = _gated_outputs(M, inner, torch.uint8, a.device, q, gu, save)
-    scales = _scales_out(M, inner, a.device, scales)
+    q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
+    scales = _scales_out(M, inner, a, scales)
     mode = _accum_code(accum, torch.bfloat16)
     ws, nbytes = _workspace((_lib or lib()).fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, w.shape[0]), workspace,
                             a.device, stream)
