@@ -174,6 +174,25 @@ def test_grouped(gpu, tokens, counts, accum):
         _check_all(ref, accum, h32[lo:hi], what=f"expert {e} f32")
 
 
+# few rows on wide experts: the small workgroup shapes, by the rows of an expert
+@pytest.mark.parametrize("accum", ["fp8", "exact", "scaled"])
+@pytest.mark.parametrize("counts,inner,K", [([1], 2048, 2048), ([0, 2, 0], 2048, 1024), ([22], 4096, 512),
+                                            ([25], 8192, 512), ([0, 38], 8192, 512), ([40], 8192, 512)])
+def test_grouped_workgroup_shapes(gpu, counts, inner, K, accum):
+    G, R, tokens = len(counts), sum(counts), 16
+    say(f"gated experts {counts} {inner}x{K} {accum}")
+    qa, sa, qw, sw = _operands(gpu, tokens, inner, K, accum == "scaled", G=G)
+    off = _segments(counts).to(gpu)
+    idx = torch.randint(0, tokens, (R,), generator=torch.Generator().manual_seed(4), dtype=torch.int32).to(gpu)
+    h, gu = layer.fp8_block_grouped_gated_gemm(qa, sa, off, qw, sw, row_index=idx, accum=accum, save=True)
+    h32 = layer.fp8_block_grouped_gated_gemm(qa, sa, off, qw, sw, row_index=idx, accum=accum, out_dtype=torch.float32)
+    q, s, gq = layer.fp8_block_grouped_gated_gemm_quant(qa, sa, off, qw, sw, row_index=idx, accum=accum, save=True)
+    e = next(i for i, c in enumerate(counts) if c)  # (one expert holds every row here)
+    ref = _reference(qa[idx.long()], sa[idx.long()], qw[e], sw[e], accum)
+    _check_all(ref, accum, h, gu, what=f"{counts}")
+    _check_all(ref, accum, h32, gq, (q, s), what=f"{counts} f32/quant")
+
+
 def test_row_index_is_clamped(gpu):
     """Indices outside the tokens read a token all the same (rows unspecified, others untouched)."""
     qa, sa, qw, sw = _operands(gpu, 4, 128, 128, False, G=2)
