@@ -25,7 +25,6 @@ remaining rows of the path and print their own JSON line; the default run prints
 """
 
 import argparse
-import hashlib
 import json
 import os
 import sys
@@ -39,21 +38,16 @@ PEAK_FP16_TFLOPS = 2500.0  # dense fp16/bf16 matrix-core peak (exact accumulatio
 PEAK_HBM_GBS = 8000.0      # MI355X HBM3E
 
 
-def _sha(path):
-    with open(path, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
-
-
 def _traffic(record_name, kernel_src):
     """HBM bytes per launch from a committed rocprofv3 counter summary, or None.
 
     The summary records the sha256 of the kernel source it was taken with; if
     the source has changed since, the figure no longer applies and None is
     returned."""
-    from fp8_fine_grained_amd.profile_summary import load_traffic
+    from fp8_fine_grained_amd.profile_summary import load_traffic, source_sha
 
     rec = load_traffic(os.path.join(ROOT, "profiles", record_name))
-    if not rec or rec.get("kernel_source_sha256") != _sha(kernel_src):
+    if not rec or rec.get("kernel_source_sha256") != source_sha(kernel_src):
         return None
     return rec.get("per_launch_bytes")
 
@@ -63,11 +57,11 @@ def _mfma_counters(record_name):
     summary (MFMA-busy fraction of the active cycles, the average clock, and
     their product over the 2.4 GHz of the published peak), or None when the
     GEMM source has changed since the counters were taken."""
-    from fp8_fine_grained_amd.profile_summary import load_traffic
+    from fp8_fine_grained_amd.profile_summary import load_traffic, source_sha
 
     src = os.path.join(ROOT, "fp8_fine_grained_amd", "csrc", "gemm_fp8.hip")
     rec = load_traffic(os.path.join(ROOT, "profiles", record_name))
-    if not rec or rec.get("kernel_source_sha256") != _sha(src):
+    if not rec or rec.get("kernel_source_sha256") != source_sha(src):
         return None
     return {"mfma_busy_fraction": rec["mfma_busy_fraction"], "clock_ghz": rec["clock_ghz"],
             "fraction_of_peak_mfma_cycles": rec["fraction_of_peak_mfma_cycles"], "source": "profiles/" + record_name}

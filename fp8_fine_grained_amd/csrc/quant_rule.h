@@ -1,5 +1,5 @@
 // The per-group quantisation rule, shared by the quantisers (quant.hip) and the
-// GEMM epilogue that writes its output already quantised (gemm_fp8.hip).
+// GEMM epilogue that writes its output already quantised (gemm_fp8_tile.h).
 // Per group (innerforce DeepSeek-V3 notes, Figure 7(a) passage; tonho.wtf
 // "DeepSeek-V3", "como funciona"):
 //     amax = max|x|,  s = fl32(amax/448),  inv = s ? fl32(1/s) : 0,

@@ -20,14 +20,16 @@ cycles over the dispatch's duration) and the matrix-core flop rate.
 over the dispatches whose name contains the substring, and scales each by what
 the same counter reads for a plain device-to-device copy of 1 GiB (the largest
 dispatch of the calibration run): bytes = counter * 1024 * (known / measured).
-The summary records the sha256 of the kernel source it was measured with;
+The summary records the sha256 of the kernel source (and of the kernel headers it
+includes) that it was measured with;
 ``bench.py`` only reports the traffic while that source is unchanged.
 """
 
 import csv
 import hashlib
-import os
 import json
+import os
+import re
 import sys
 
 COPY_BYTES = 1 << 30
@@ -36,6 +38,18 @@ COPY_BYTES = 1 << 30
 def _rows(path):
     with open(path) as f:
         return list(csv.DictReader(f))
+
+
+def source_sha(path):
+    """sha256 of a kernel source and of the kernel headers (``*_tile.h`` beside it)
+    that it includes."""
+    with open(path, "rb") as f:
+        text = f.read()
+    digest = hashlib.sha256(text)
+    for name in re.findall(rb'^#include "(\w+_tile\.h)"', text, flags=re.M):
+        with open(os.path.join(os.path.dirname(path), name.decode()), "rb") as f:
+            digest.update(f.read())
+    return digest.hexdigest()
 
 
 def _bench_line(log_path):
@@ -127,8 +141,7 @@ def traffic(fetch_csv, write_csv, cal_fetch_csv, cal_write_csv, substr, kernel_s
     w_scale = COPY_BYTES / (cw_kib * 1024.0)
     fetch_bytes = f_kib * 1024.0 * f_scale
     write_bytes = w_kib * 1024.0 * w_scale
-    with open(kernel_src, "rb") as fh:
-        sha = hashlib.sha256(fh.read()).hexdigest()
+    sha = source_sha(kernel_src)
     rec = {
         "kernel": name[:200],
         "kernel_source": kernel_src,
@@ -237,8 +250,7 @@ def mfma(csv_path, substr, last_n, kernel_src, out_md, command):
         lines.append(f"| FP8 matrix-core work = MOPS_F8 x 512 | {flops8 / 1e9:.1f} GFLOP, {flops8 / t_s / 1e12:.0f} TFLOP/s |")
     if flops16:
         lines.append(f"| F16 matrix-core work = MOPS_F16 x 512 | {flops16 / 1e9:.1f} GFLOP, {flops16 / t_s / 1e12:.0f} TFLOP/s |")
-    with open(kernel_src, "rb") as fh:
-        sha = hashlib.sha256(fh.read()).hexdigest()
+    sha = source_sha(kernel_src)
     rec = {"kernel": name[:200], "kernel_source": kernel_src, "kernel_source_sha256": sha,
            "dispatches_averaged": len(ds), "duration_us": t_s * 1e6, "mfma_busy_fraction": util,
            "clock_ghz": clock, "fraction_of_peak_mfma_cycles": util * clock / PEAK_CLOCK_GHZ}
