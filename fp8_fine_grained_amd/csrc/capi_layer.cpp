@@ -191,8 +191,8 @@ int fp8_block_grouped_gated_gemm(const uint8_t* a, const float* sa, int64_t T, c
                                  const int32_t* group_offsets, int64_t G, const uint8_t* w, const float* sw,
                                  int accum, void* h, int h_dtype, void* gu, int64_t M_total, int64_t I, int64_t K,
                                  fp8fg_stream_t stream) {
-  return grouped_gated(a, sa, T, row_index, group_offsets, G, w, sw, accum, h, h_dtype, nullptr, 0, gu, nullptr, M_total,
-                       I, K, stream);
+  return grouped_gated(a, sa, T, row_index, group_offsets, G, w, sw, accum, h, h_dtype, nullptr, 0, gu, nullptr,
+                       M_total, I, K, stream);
 }
 
 int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_t T, const int32_t* row_index,

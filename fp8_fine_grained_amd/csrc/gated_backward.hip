@@ -19,7 +19,8 @@ struct Grads {
   float g[8], u[8], h[8];
   // dh, gate and up octets as loaded
   using O = Octet<BF16>;
-  __device__ __forceinline__ void form(const typename O::Raw& rd, const typename O::Raw& rg, const typename O::Raw& ru) {
+  __device__ __forceinline__ void form(const typename O::Raw& rd, const typename O::Raw& rg,
+                                       const typename O::Raw& ru) {
     float d[8];
     O::widen(rd, d);
     O::widen(rg, g);

@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   static_assert(!(ROWS && GROUPED), "grouped weights carry block scales");
   static_assert(!GATHER || GROUPED, "gathering is a grouped-GEMM mode");
   static_assert(!SCALED || (!EXACT && !ROWS), "the scaled mode takes FP8 products and 128x128 weight scales");
-  static_assert(QOUT == 0 || GATED || (TN == 128 && BALIGN && !GROUPED), "a wavefront's row of the tile is one 1x128 group");
+  static_assert(QOUT == 0 || GATED || (TN == 128 && BALIGN && !GROUPED),
+                "a wavefront's row of the tile is one 1x128 group");
   constexpr int HALF = TN / 2;  // gated: a wavefront's output columns
   static_assert(!GATED || (BN == 256 && !ROWS && !B_RR && SN % 2 == 0 && HALF % (BN / NW) == 0),
                 "gated tiles: 128 output columns (one 1x128 group), whole gate or up rows per wavefront's DMAs");
@@ -1005,7 +1006,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
             dma_slot(i, j);
             if (i > 0) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[i - 1][j][r] = fmaf(P[(i - 1) & 1][j][r], up_half(i - 1) ? fu[j] : f[j], acc[i - 1][j][r]);
+              for (int r = 0; r < 4; ++r)
+                acc[i - 1][j][r] = fmaf(P[(i - 1) & 1][j][r], up_half(i - 1) ? fu[j] : f[j], acc[i - 1][j][r]);
             } else if (DEFER && kb > 0) {
 #pragma unroll
               for (int r = 0; r < 4; ++r)
@@ -1066,7 +1068,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
         int ex_old[SMW];
 #pragma unroll
         for (int j = 0; j < SMW; ++j) ex_old[j] = ex[j];
-        read_block_nfirst(st, [&](int j) { acc[SN - 1][j] = mma_scaled(fn_old, fm[j], acc[SN - 1][j], ew_old, ex_old[j]); });
+        read_block_nfirst(
+            st, [&](int j) { acc[SN - 1][j] = mma_scaled(fn_old, fm[j], acc[SN - 1][j], ew_old, ex_old[j]); });
         continue;
       }
       float f_old[SMW];

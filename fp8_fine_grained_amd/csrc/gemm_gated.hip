@@ -38,13 +38,17 @@ hipError_t launch_tiles(const GemmArgs& g, hipStream_t s) {
   p.T_full = static_cast<int>(MT * p.NT);
   p.split = 1;
   const dim3 grid(static_cast<unsigned>(p.T_full)), block(C::WM * C::WN * 64);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, p); };
+  auto go = [&](auto bf16, auto quantised) {
+    hipLaunchKernelGGL((gemm_fp8_block_kernel<C::BM, C::BN, C::WM, C::WN, C::ST, EXACT, false, decltype(bf16)::value,
+                                              GROUPED, GROUPED, SCALED, decltype(quantised)::value ? 3 : 0, true>),
+                       grid, block, 0, s, p);
+  };
   if (g.y_scales)
-    go(gemm_fp8_block_kernel<C::BM, C::BN, C::WM, C::WN, C::ST, EXACT, false, false, GROUPED, GROUPED, SCALED, 3, true>);
+    go(std::false_type{}, std::true_type{});
   else if (g.y_bf16)
-    go(gemm_fp8_block_kernel<C::BM, C::BN, C::WM, C::WN, C::ST, EXACT, false, true, GROUPED, GROUPED, SCALED, 0, true>);
+    go(std::true_type{}, std::false_type{});
   else
-    go(gemm_fp8_block_kernel<C::BM, C::BN, C::WM, C::WN, C::ST, EXACT, false, false, GROUPED, GROUPED, SCALED, 0, true>);
+    go(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 
@@ -313,8 +317,9 @@ struct Shape {
   int cols, rows;
   float start, per_block;
 };
-constexpr Shape kShapes[] = {{8, 16, 0.8f, 0.073f},  {16, 16, 0.5f, 0.14f}, {32, 16, 0.7f, 0.19f}, {16, 32, 0.9f, 0.155f},
-                             {32, 32, 1.8f, 0.22f},  {32, 64, 2.9f, 0.32f}, {128, 128, 2.1f, 1.0f}, {128, 256, 1.9f, 1.6f}};
+constexpr Shape kShapes[] = {{8, 16, 0.8f, 0.073f},  {16, 16, 0.5f, 0.14f}, {32, 16, 0.7f, 0.19f},
+                             {16, 32, 0.9f, 0.155f}, {32, 32, 1.8f, 0.22f}, {32, 64, 2.9f, 0.32f},
+                             {128, 128, 2.1f, 1.0f}, {128, 256, 1.9f, 1.6f}};
 constexpr int kTile128 = 6, kTile256 = 7;
 
 template <int MODE>
@@ -395,7 +400,8 @@ hipError_t launch_gated_gemm(const GemmArgs& g, float* workspace, hipStream_t s)
   f.gu_bf16 = true;
   const hipError_t e = launch_shape(f, shape, s);
   if (e != hipSuccess) return e;
-  return launch_quant_act_rows(workspace, false, g.pow2, g.M, g.N / 2, g.N / 2, static_cast<uint8_t*>(g.y), g.y_scales, s);
+  return launch_quant_act_rows(workspace, false, g.pow2, g.M, g.N / 2, g.N / 2, static_cast<uint8_t*>(g.y),
+                               g.y_scales, s);
 }
 
 }  // namespace fp8fg

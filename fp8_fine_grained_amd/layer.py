@@ -236,8 +236,9 @@ def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=N
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw, M)
     h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
-    st = (_lib or lib()).fp8_block_gated_gemm(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h),
-                                    _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream, a))
+    st = (_lib or lib()).fp8_block_gated_gemm(
+        _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu),
+        M, inner, K, _stream(stream, a))
     _check("fp8_block_gated_gemm", st)
     return h if gu is None else (h, gu)
 
@@ -251,9 +252,11 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
     scales = _scales_out(M, inner, a, scales)
     mode = _accum_code(accum, torch.bfloat16)
-    ws, nbytes = _workspace((_lib or lib()).fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device, stream)
-    st = (_lib or lib()).fp8_block_gated_gemm_quant(_ptr(a), _ptr(sa), _ptr(w), _ptr(sw), mode, 1 if pow2 else 0, _ptr(q),
-                                          _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream, a))
+    L = _lib or lib()
+    ws, nbytes = _workspace(L.fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device, stream)
+    st = L.fp8_block_gated_gemm_quant(
+        _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), mode, 1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws),
+        nbytes, M, inner, K, _stream(stream, a))
     _check("fp8_block_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
 
@@ -294,9 +297,10 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
     scales = _scales_out(M, inner, a, scales)
     mode = _accum_code(accum, torch.bfloat16)
-    ws, nbytes = _workspace((_lib or lib()).fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, w.shape[0]), workspace,
+    L = _lib or lib()
+    ws, nbytes = _workspace(L.fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, w.shape[0]), workspace,
                             a.device, stream)
-    st = (_lib or lib()).fp8_block_grouped_gated_gemm_quant(
+    st = L.fp8_block_grouped_gated_gemm_quant(
         _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw), mode,
         1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream, a))
     _check("fp8_block_grouped_gated_gemm_quant", st)
@@ -327,8 +331,9 @@ def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_colu
                 torch.empty((n, k // 128), dtype=torch.float32, device=dh.device))
 
     out = (*pair(rows, M, 2 * inner), *pair(columns, 2 * inner, M), *pair(h_columns, inner, M))
-    st = (_lib or lib()).fp8_gated_backward_quant(_ptr(dh), _ptr(gu), _dtype_code(dh.dtype), M, inner, _ld(dh), 1 if pow2 else 0,
-                                        *[_ptr(t) for t in out], _stream(stream, dh))
+    st = (_lib or lib()).fp8_gated_backward_quant(
+        _ptr(dh), _ptr(gu), _dtype_code(dh.dtype), M, inner, _ld(dh), 1 if pow2 else 0, *[_ptr(t) for t in out],
+        _stream(stream, dh))
     _check("fp8_gated_backward_quant", st)
     return out
 
