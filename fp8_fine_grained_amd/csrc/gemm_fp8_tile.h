@@ -556,12 +556,17 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
   // The fp32-scale dense tiles with block scales issue each DMA right after
   // one MFMA (the interleaved issue described in the K loop).
   constexpr bool ILV_DENSE = !GROUPED && !SCALED && !EXACT && !ROWS && BALIGN && NW == 8 && SN >= 8;
+  // Tiles with 64-column wavefronts that take the grouped schedule below (fragments
+  // two steps ahead, deferred promotion, interleaved issue): the grouped ones, and the
+  // dense gated ones (512 x 2048 x 7168: FP8 60.5 -> 47.9 us, scaled 52.6 -> 46.5; the
+  // exact ones lost 3% and stay as they were).
+  constexpr bool NARROW = GROUPED || (GATED && !EXACT && SN == 4);
   // Sub-tile steps that issue the DMAs: four of eight for those tiles (their
   // GEMM on 4096 x 7168 x 7168: 187.9 us over six steps, 185.7 over four, 185.3
   // over two, 188.7 in one), six of eight for the other 256 x 256 tiles, three
   // of four for the grouped ones (1.6% faster on the MoE shape than two, which
   // the row-scaled weight-gradient tiles keep: three is 1-8% slower there)
-  constexpr int SPREAD = ILV_DENSE ? 4 : (SN >= 7 ? SN - 2 : (SN >= 4 ? (GROUPED ? SN - 1 : SN / 2) : SN));
+  constexpr int SPREAD = ILV_DENSE ? 4 : (SN >= 7 ? SN - 2 : (SN >= 4 ? (NARROW ? SN - 1 : SN / 2) : SN));
   static_assert(SPREAD < SN, "every tile DMA of a stage is issued before the stage's last step");
   auto dma_tile = [&](int d, int kb, int st) {
     const int64_t kof = static_cast<int64_t>(kb_begin + kb) * 128;
@@ -785,7 +790,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     // next one): 2% faster on the MoE shape, where a step is 4 MFMAs; the dense
     // tiles read one step ahead (two ahead measured 1.5% slower with eight
     // wavefronts and 18% slower with four).
-    constexpr bool FD2 = GROUPED && SN > 2;
+    constexpr bool FD2 = NARROW && SN > 2;
     v8i fn, fn1;
     // Scaled mode: E8M0 codes (the fp32 exponent field) of the lane's act-row
     // scale in each m sub-tile, and of the wavefront's weight-block scale.
@@ -923,7 +928,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     // not rewritten before then: step 0 writes the other buffer).  1.8% faster on
     // the MoE shape; 1% slower on the dense 256 x 256 tile, which keeps the
     // immediate promotion.
-    constexpr bool DEFER = GROUPED && !SCALED && BALIGN;
+    constexpr bool DEFER = NARROW && !SCALED && BALIGN;
     static_assert(!DEFER || SN % 2 == 0, "the deferred partials use the buffer step 0 does not write");
     // Interleaved issue (the four-wavefront power-of-two tiles, the grouped FP8
     // tiles and the fp32-scale dense tiles with block scales): the step's tile
@@ -939,7 +944,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
     // with an earlier DMA spread (four steps instead of six: 188.8 -> 187.4 and
     // 187.9 -> 185.7 us; with six, 189.3 vs 189.5).  The exact tiles (weight
     // gradient 1609 vs 1630 us) gain nothing and keep the compiler's order.
-    constexpr bool ILV = (SCALED && NW == 4) || (GROUPED && !SCALED && !EXACT) || ILV_DENSE;
+    constexpr bool ILV = (SCALED && NW == 4) || (NARROW && !SCALED && !EXACT) || ILV_DENSE;
     static_assert(!ILV || SCALED || !ROWS, "the interleaved promotion is the block-scale form");
     static_assert(!ILV || PF == 0 || SPREAD <= SN - 2, "the L2 prefetch stays each iteration's newest load");
     float f_prev[SMW];

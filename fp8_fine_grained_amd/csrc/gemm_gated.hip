@@ -346,11 +346,11 @@ hipError_t launch_mode(const GemmArgs& g, int shape, hipStream_t s) {
 // The shape of the least estimated time: rounds of the compute units times the
 // time of a round.  The times are fitted to every shape measured on 290 problems
 // (256 units; FP8 and exact sums; weights from 0.5 to 900 MB, 1 to 8192 rows, up
-// to 256 experts); the choice then costs 0.9% over the best shape of each dense
-// problem on average (25% at worst) and 4% with experts, where the rows of each
-// are unknown here.  Against the tile kernel alone: one token of 2048 x 7168 7.6
-// instead of 83 us, 64 rows 13 instead of 92; against 256-row tiles alone: 777
-// rows 59 instead of 87.
+// to 256 experts); the choice then costs 0.4% over the best shape of each dense FP8
+// or scaled problem on average (10% at worst) and 4% with experts, where the rows of
+// each are unknown here.  Against the tile kernel alone: one token of 2048 x 7168 7.6
+// instead of 83 us, 64 rows 13 instead of 90; against 256-row tiles alone: 777
+// rows 50 instead of 88.
 int choose_shape(const GemmArgs& g, bool tiles_only) {
   const int found = device_cus();
   const double cus = found > 0 ? found : 256;
