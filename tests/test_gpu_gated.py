@@ -297,6 +297,28 @@ def test_gradient_strides_bounds_and_extremes(gpu):
         assert torch.all(r[1][4] == 0) and torch.all(r[0][4] & 0x7F == 0)
 
 
+def test_gradient_at_huge_gates(gpu):
+    """Gates up to the largest finite values: the sigmoid is 1 above and 0 below, and
+    nothing turns into NaN on the way there.  (dh and u of the large positive ones
+    are 1/2, so that every output is finite.)"""
+    M, inner = 128, 256
+    huge = [90.0, 1e3, 1e6, 1e10, 1e20, 1e30, 3e38]
+    for dtype in (torch.bfloat16, torch.float32):
+        dh, gu = _grad_inputs(M, inner, dtype)
+        for i, v in enumerate(huge):
+            gu[i, 5 + i] = -v                    # among ordinary values
+            gu[8 + i, 128:inner] = v             # a group of one huge value
+            gu[8 + i, inner + 128:] = 0.5
+            dh[8 + i, 128:] = 0.5
+        ref, floor, h = _grad_reference(dh, gu)
+        rows = layer.fp8_gated_backward_quant(dh.to(gpu), gu.to(gpu), columns=False, h_columns=False)
+        r = layer.fp8_gated_backward_quant(dh.to(gpu), gu.to(gpu))
+        for q, s in (rows[:2], r[:2]):
+            check_quant(q, s, ref, 4 * U, False, "rows", floor)
+        check_quant(r[2], r[3], ref.t().contiguous(), 4 * U, False, "columns", floor.t().contiguous())
+        check_quant(r[4], r[5], h.t().contiguous(), 20 * U, False, "h columns")
+
+
 def test_gradient_against_differences(gpu):
     """The dequantised codes against central differences of the 64-bit activation:
     within half an E4M3 step (1/16 of the value, or 2^-10 of the scale) and 1e-6."""
