@@ -723,6 +723,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 1) gemm_fp8_block_kernel(FParams
           group_scale<true>(a, sc, inv);
         else
           group_scale<false>(a, sc, inv);
+        if (sc < 0x1p-126f) inv = 0.0f;  // gates so far below zero that 1/sc may be infinite: zero codes
 #pragma unroll
         for (int i = 0; i < SH; ++i)
           *reinterpret_cast<uint32_t*>(epi + mr * QP + i * 16 + 4 * (lane >> 4)) =

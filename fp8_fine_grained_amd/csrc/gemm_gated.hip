@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "gemm_fp8_tile.h"
+#include "lanes.h"
 
 namespace fp8fg {
 namespace {
@@ -310,6 +311,21 @@ hipError_t launch_split(const GemmArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The 1x128 quantisation of h [M, I] (fp32) that the small tiles left in the
+// workspace: 16 lanes per group, by the rule that the tiles' own epilogue follows.
+__global__ void __launch_bounds__(256) gated_quant_kernel(const float* __restrict__ h, int64_t groups, bool pow2,
+                                                          uint8_t* __restrict__ q, float* __restrict__ scales) {
+  using O = Octet<false>;
+  const int part = threadIdx.x & 15;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (t >= groups) return;  // 16 whole lanes; only those exchange below
+  float v[8], s, inv;
+  O::widen(O::load(reinterpret_cast<const char*>(h + t * 128), part), v);
+  group_scale(pow2, group_amax(v), s, inv);
+  O::store_codes(q + t * 128, part, v, inv);
+  if (part == 0) scales[t] = s;
+}
+
 // The workgroup shapes: output columns and rows, and the time of one round of the
 // compute units, start + per_block * K/128 (us).  The last two are the tile
 // kernel's 128 x 256 and 256 x 256 tiles, the others the kernel above.
@@ -400,8 +416,10 @@ hipError_t launch_gated_gemm(const GemmArgs& g, float* workspace, hipStream_t s)
   f.gu_bf16 = true;
   const hipError_t e = launch_shape(f, shape, s);
   if (e != hipSuccess) return e;
-  return launch_quant_act_rows(workspace, false, g.pow2, g.M, g.N / 2, g.N / 2, static_cast<uint8_t*>(g.y),
-                               g.y_scales, s);
+  const int64_t groups = g.M * (g.N / 256);
+  hipLaunchKernelGGL(gated_quant_kernel, dim3(static_cast<unsigned>((groups + 15) / 16)), dim3(256), 0, s, workspace,
+                     groups, g.pow2, static_cast<uint8_t*>(g.y), g.y_scales);
+  return hipGetLastError();
 }
 
 }  // namespace fp8fg

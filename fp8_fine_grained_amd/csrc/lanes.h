@@ -121,7 +121,9 @@ __device__ __forceinline__ float group_amax(const float (&f)[8]) {
 // is its product with the rounded reciprocal plus one correction, and 1/s one
 // Newton step on the hardware reciprocal (both equal to the correctly rounded
 // divisions for every amax of the rule's range, checked over all mantissas and
-// exponents).
+// exponents).  Below that range (s under the smallest normal, where 1/s may be
+// infinite) the codes are zero: the caller of a fused operator does not see the
+// values that are quantised, and cannot keep them out of it.
 __device__ __forceinline__ void group_scale(bool pow2, float amax, float& s, float& inv) {
   if (pow2) {
     group_scale<true>(amax, s, inv);
@@ -131,7 +133,7 @@ __device__ __forceinline__ void group_scale(bool pow2, float amax, float& s, flo
   const float q = amax * kInv448;
   s = fmaf(fmaf(-kE4M3Max, q, amax), kInv448, q);
   const float r = __builtin_amdgcn_rcpf(s);
-  inv = s == 0.0f ? 0.0f : fmaf(fmaf(-s, r, 1.0f), r, r);
+  inv = s < 0x1p-126f ? 0.0f : fmaf(fmaf(-s, r, 1.0f), r, r);
 }
 
 }  // namespace fp8fg

@@ -27,7 +27,8 @@ extern "C" {
  *     h = z rounded to `dtype`, for the residual stream and the backward pass.
  * y comes from the unrounded z.  z^2 is summed in fp32, so |z| beyond about 1e19
  * is outside the range; other finite inputs are fine.  A row of zeros gives zero
- * codes and scales.
+ * codes and scales; a group whose largest |y| lies below 448 * 2^-126 gives
+ * zero codes, or with pow2 codes at the smallest normal scale.
  *
  * x, residual  [M, H] of `dtype`, row pitches ld_x, ld_r >= H elements; residual
  *              may be NULL (then z = x).
@@ -85,7 +86,9 @@ int fp8_block_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, co
 
 /*
  * The same with h leaving 1x128-quantised along I (rule of fp8_quant_act_1x128, or
- * of fp8_quant_act_1x128_pow2 with pow2 == 1), ready for the down projection.
+ * of fp8_quant_act_1x128_pow2 with pow2 == 1), ready for the down projection.  A
+ * group whose largest |h| lies below 448 * 2^-126 gives zero codes, or with pow2
+ * codes at the smallest normal scale.
  * q_h, s_h     out, codes [M, I] (16-byte aligned) and fp32 [M, I/128].
  * gu           out, bf16 [M, 2I], or NULL.
  * workspace    4 * M * I bytes, 16-byte aligned, or NULL.  With few rows the work is
@@ -131,7 +134,9 @@ int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_
  *                 of it with the transposed quantisation of X.
  *     q_ht, s_ht  [I, M], [I, M/128]: h transposed, quantised along the tokens, for
  *                 the down projection's dW.
- * Quantisation by the rule of fp8_quant_act_1x128, or of its _pow2 form.
+ * Quantisation by the rule of fp8_quant_act_1x128, or of its _pow2 form; a group whose
+ * largest value lies below 448 * 2^-126 (saturated gates, say) has zero codes, or with
+ * pow2 codes at the smallest normal scale.
  *
  * dh           [M, I] of `dtype`, row pitch ld_dh >= I.
  * gu           [M, 2I] of `dtype`, as the forward call saved it.

@@ -135,6 +135,31 @@ def test_large_gates(gpu):
         _check_all(_reference(qa, sa, qw, sw, accum), accum, h, what=f"large {accum}")
 
 
+@pytest.mark.parametrize("M,accum", [(1, "fp8"), (20, "exact"), (300, "fp8"), (300, "exact"), (300, "scaled")])
+def test_gates_far_below_zero_quantised(gpu, M, accum):
+    """The gates of a group at -88 and -123, where |h| is below the quantisers' range or zero: the
+    codes are zeros, not NaN; the other group is quantised as ever.  With and without the workspace."""
+    inner, K = 256, 256
+    gen = torch.Generator().manual_seed(M)
+    x = (1 + 0.002 * torch.rand((M, 1), generator=gen)).expand(M, K).contiguous()
+    w = torch.randn((2 * inner, K), generator=gen) / K ** 0.5
+    w[:128] = -88 / 256
+    w[7:128:2] *= 1.4  # (320 and 448 times the scale: both exact)
+    pow2 = accum == "scaled"
+    qa, sa = binding.fp8_quant_act_1x128(x.to(gpu), pow2=pow2)
+    qw, sw = binding.fp8_quant_weight_128x128(w.to(gpu), pow2=pow2)
+    ref = _reference(qa, sa, qw, sw, accum)
+    assert -88.5 < float(ref[0][:, :128].max()) < -87 and float(ref[0][:, :128].min()) < -103
+    h = silu(ref[0]) * ref[1]
+    assert float(h[:, :128].abs().max()) < 448 * 2.0 ** -126
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=gpu)):
+        q, s = layer.fp8_block_gated_gemm_quant(qa, sa, qw, sw, accum=accum, workspace=ws)
+        assert torch.all(q[:, :128] & 0x7F == 0) and torch.all(s[:, 0] < 2.0 ** -126)
+        floor = gated_bound(*ref, 64 * U)[:, 128:].contiguous()
+        check_quant(q[:, 128:].contiguous(), s[:, 1:].contiguous(), h[:, 128:].contiguous(), 2 * U, False, "others",
+                    floor=floor)
+
+
 def _segments(counts):
     return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
 
@@ -317,6 +342,23 @@ def test_gradient_at_huge_gates(gpu):
             check_quant(q, s, ref, 4 * U, False, "rows", floor)
         check_quant(r[2], r[3], ref.t().contiguous(), 4 * U, False, "columns", floor.t().contiguous())
         check_quant(r[4], r[5], h.t().contiguous(), 20 * U, False, "h columns")
+
+
+def test_gradient_groups_below_the_normal_range(gpu):
+    """Gradients of saturated gates may underflow: zero codes there, no NaN, in every output."""
+    M, inner = 128, 256
+    for dtype in (torch.bfloat16, torch.float32):
+        dh, gu = _grad_inputs(M, inner, dtype)
+        gu[:, :128] = -84.0  # p about 3e-37, and dh about 1e-3
+        gu[0, 3] = 0
+        gu[:, inner] = 0
+        q, s, qt, st, qht, sht = layer.fp8_gated_backward_quant(dh.to(gpu), gu.to(gpu))
+        for codes in (q, qt, qht):
+            assert not torch.any(codes & 0x7F == 0x7F)
+        assert torch.all(q[1:, :128] & 0x7F == 0) and torch.all(s[1:, 0] < 2.0 ** -126)
+        assert torch.all(qt[:3] & 0x7F == 0) and torch.all(st[:3] < 2.0 ** -126)
+        rows = layer.fp8_gated_backward_quant(dh.to(gpu), gu.to(gpu), columns=False, h_columns=False)
+        assert torch.equal(rows[0], q) and torch.equal(rows[1], s)
 
 
 def test_gradient_against_differences(gpu):

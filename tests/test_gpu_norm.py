@@ -111,6 +111,20 @@ def test_zero_rows_and_extreme_values(gpu):
     assert dx.shape == (0, H) and torch.all(dw == 0)
 
 
+def test_groups_below_the_normal_range(gpu):
+    """Weights that leave a group's largest |y| below 448 * 2^-126: codes of value zero, no NaN,
+    and the other groups as always."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x, r, w = _inputs(3, 512, dtype)
+        x[:, 5] = r[:, 5] = 0  # a zero among the tiny values
+        w[:128] = 1e-38
+        w[128:256] = 3e-38
+        _, q, s, _ = layer.fp8_add_rmsnorm_quant_1x128(x.to(gpu), w.to(gpu), residual=r.to(gpu))
+        assert torch.all(q[:, :256] & 0x7F == 0) and torch.all(s[:, :2] < 2.0 ** -126)
+        y = _forward_ref(x, r, w)[2]
+        check_quant(q[:, 256:].contiguous(), s[:, 2:].contiguous(), y[:, 256:].contiguous(), REL_Y, False, "others")
+
+
 def test_eps_zero_and_large(gpu):
     x, _, w = _inputs(3, 256, torch.float32)
     for eps in (0.0, 10.0):
