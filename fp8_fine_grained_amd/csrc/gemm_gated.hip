@@ -367,7 +367,8 @@ hipError_t launch_mode(const GemmArgs& g, int shape, hipStream_t s) {
 // each are unknown here.  Against the tile kernel alone: one token of 2048 x 7168 7.6
 // instead of 83 us, 64 rows 13 instead of 90; against 256-row tiles alone: 777
 // rows 50 instead of 88.
-int choose_shape(const GemmArgs& g, bool tiles_only) {
+// Quantised outputs of the small tiles take a second launch, 3 us.
+int choose_shape(const GemmArgs& g, bool quantised, bool tiles_only) {
   const int found = device_cus();
   const double cus = found > 0 ? found : 256;
   const int64_t I = g.N / 2, KB = g.K / 128;
@@ -385,7 +386,8 @@ int choose_shape(const GemmArgs& g, bool tiles_only) {
     double per_block = t.per_block;
     if (i == kTile128) per_block *= (g.exact ? 1.55 : 1.0) * (rows <= 64 ? 0.7 : 1.0);
     const double wgs = static_cast<double>(groups * ((rows + t.rows - 1) / t.rows)) * ((I + t.cols - 1) / t.cols);
-    const double time = std::ceil(wgs / cus) * (t.start + KB * per_block);
+    double time = std::ceil(wgs / cus) * (t.start + KB * per_block);
+    if (quantised && i < kTile128) time += 3.0;
     if (least == 0 || time < least) {
       least = time;
       best = i;
@@ -401,11 +403,11 @@ hipError_t launch_shape(const GemmArgs& g, int shape, hipStream_t s) {
 
 }  // namespace
 
-bool gated_quant_takes_workspace(const GemmArgs& g) { return choose_shape(g, false) < kTile128; }
+bool gated_quant_takes_workspace(const GemmArgs& g) { return choose_shape(g, true, false) < kTile128; }
 
 hipError_t launch_gated_gemm(const GemmArgs& g, float* workspace, hipStream_t s) {
-  if (!g.y_scales) return launch_shape(g, choose_shape(g, false), s);
-  const int shape = choose_shape(g, workspace == nullptr);
+  if (!g.y_scales) return launch_shape(g, choose_shape(g, false, false), s);
+  const int shape = choose_shape(g, true, workspace == nullptr);
   if (shape >= kTile128) return launch_shape(g, shape, s);
   // Small tiles do not hold whole 1x128 groups: h goes through the workspace in
   // fp32 and is quantised by a second launch.
