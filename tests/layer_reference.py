@@ -46,7 +46,7 @@ def check_quant(q, scales, ref, rel, pow2=False, what="", floor=None):
     _, e = torch.frexp(v.abs() + off)
     step = torch.exp2((e - 1).clamp(min=-6).double() - 3)
     tol = step / 2 + off
-    bad = ((q - v).abs() > tol) & (s > 0)[:, :, None]
+    bad = ~((q - v).abs() <= tol) & (s > 0)[:, :, None]  # (a NaN is within no bound)
     assert not bad.any(), f"{what}: {int(bad.sum())} codes off, first {bad.nonzero()[:3].tolist()}"
     assert torch.all(q[s == 0] == 0), f"{what}: codes of a zero group"
 
