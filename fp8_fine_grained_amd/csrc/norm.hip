@@ -97,7 +97,10 @@ __global__ void __launch_bounds__(norm_rows(WPR) * WPR * 64) rmsnorm_quant_kerne
     for (int w = 0; w < WPR; ++w) ss += partial[slot * WPR + w];
   }
   if (!live) return;
-  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
+  // A row of zeros without eps (or one whose squares vanish in fp32) has no direction:
+  // zero, not 0 * infinity, here and, through rstd, in the gradient.
+  const float mean = ss / static_cast<float>(a.H) + a.eps;
+  const float rstd = mean == 0.0f ? 0.0f : 1.0f / sqrtf(mean);
   if (t == 0 && a.rstd) a.rstd[m] = rstd;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {

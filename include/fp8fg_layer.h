@@ -27,8 +27,11 @@ extern "C" {
  *     h = z rounded to `dtype`, for the residual stream and the backward pass.
  * y comes from the unrounded z.  z^2 is summed in fp32, so |z| beyond about 1e19
  * is outside the range; other finite inputs are fine.  A row of zeros gives zero
- * codes and scales; a group whose largest |y| lies below 448 * 2^-126 gives
- * zero codes, or with pow2 codes at the smallest normal scale.
+ * codes and scales.  With eps == 0 rstd has its full precision where mean(z^2) is
+ * at least 2^-126, and a row whose mean(z^2) is zero in fp32 (zeros, or |z| below
+ * about 1e-22) counts as a row of zeros, with rstd = 0.  A group whose largest |y|
+ * lies below 448 * 2^-126 gives zero codes, or with pow2 codes at the smallest
+ * normal scale.
  *
  * x, residual  [M, H] of `dtype`, row pitches ld_x, ld_r >= H elements; residual
  *              may be NULL (then z = x).
@@ -49,7 +52,8 @@ int fp8_add_rmsnorm_quant_1x128(const void* x, const void* residual, int dtype, 
  * Gradient of the norm (the quantisation passes gradients through unchanged):
  * with n = h * rstd and d = dy * weight,
  *     dx = rstd * (d - n * mean(d * n)) + dh,   dw = sum over rows of dy * n.
- * dx is the gradient of both x and the residual.  dw is summed in fp32, in an
+ * dx is the gradient of both x and the residual.  A row with rstd == 0 (see the
+ * forward call) has dx = dh and adds nothing to dw.  dw is summed in fp32, in an
  * order fixed by M and H alone: the same bits on every run.
  *
  * dy, h, dh    [M, H] of `dtype`, row pitches ld_* >= H; dh, the gradient that
