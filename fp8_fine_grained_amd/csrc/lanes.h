@@ -119,21 +119,23 @@ __device__ __forceinline__ float group_amax(const float (&f)[8]) {
 // The group rule with the scale form chosen at run time, and with the same bits as
 // group_scale<>() from quant_rule.h in fewer instructions: a quotient by a constant
 // is its product with the rounded reciprocal plus one correction, and 1/s one
-// Newton step on the hardware reciprocal (both equal to the correctly rounded
-// divisions for every amax of the rule's range, checked over all mantissas and
-// exponents).  Below that range (s under the smallest normal, where 1/s may be
-// infinite) the codes are zero: the caller of a fused operator does not see the
-// values that are quantised, and cannot keep them out of it.
+// Newton step on the hardware reciprocal.  (Both are then the correctly rounded
+// divisions; the tests compare them with the quantisers over every mantissa.)  An
+// infinite amax has an infinite scale and 1/s = 0, as the rule has it.  Below the
+// rule's range (s under the smallest normal, where 1/s may be infinite) the codes are
+// zero: the caller of a fused operator does not see the values that are quantised,
+// and cannot keep them out of it.
 __device__ __forceinline__ void group_scale(bool pow2, float amax, float& s, float& inv) {
   if (pow2) {
     group_scale<true>(amax, s, inv);
     return;
   }
   constexpr float kInv448 = 1.0f / kE4M3Max;
+  constexpr int kPositiveNormal = 0x100;
   const float q = amax * kInv448;
-  s = fmaf(fmaf(-kE4M3Max, q, amax), kInv448, q);
+  s = amax < __builtin_inff() ? fmaf(fmaf(-kE4M3Max, q, amax), kInv448, q) : amax;
   const float r = __builtin_amdgcn_rcpf(s);
-  inv = s < 0x1p-126f ? 0.0f : fmaf(fmaf(-s, r, 1.0f), r, r);
+  inv = __builtin_amdgcn_classf(s, kPositiveNormal) ? fmaf(fmaf(-s, r, 1.0f), r, r) : 0.0f;
 }
 
 }  // namespace fp8fg
