@@ -191,10 +191,12 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
     return dx, dw
 
 
-def _gated_operands(a, sa, w, sw, rows):
+def _gated_operands(a, sa, w, sw, experts=False):
     """Shapes of a gated product: (K, I) after checking operands against each other."""
-    K, I2 = a.shape[1], w.shape[-2]
-    lead = w.shape[:-2]
+    if a.dim() != 2 or w.dim() != (3 if experts else 2):
+        raise ValueError("a must be [rows, K], w [2I, K], or [G, 2I, K] over experts")
+    rows, K = a.shape
+    lead, I2 = w.shape[:-2], w.shape[-2]
     _given("a", torch.uint8, (rows, K), a)
     _given("sa", torch.float32, (rows, K // 128), sa)
     _given("w", torch.uint8, (*lead, I2, K), w)
@@ -234,7 +236,7 @@ def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=N
     :func:`binding.fp8_block_gemm`.  With ``save=True`` (or a ``gu`` buffer) also
     g and u [M, 2I] for the backward pass: returns ``(h, gu)``, else ``h``."""
     M = a.shape[0]
-    K, inner = _gated_operands(a, sa, w, sw, M)
+    K, inner = _gated_operands(a, sa, w, sw)
     h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
     st = (_lib or lib()).fp8_block_gated_gemm(
         _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu),
@@ -248,7 +250,7 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
     """The same with h leaving 1x128-quantised: ``(q uint8 [M, I], scales fp32 [M, I/128])``,
     and the bf16 ``gu`` [M, 2I] as a third with ``save=True``."""
     M = a.shape[0]
-    K, inner = _gated_operands(a, sa, w, sw, M)
+    K, inner = _gated_operands(a, sa, w, sw)
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
     scales = _scales_out(M, inner, a, scales)
     mode = _accum_code(accum, torch.bfloat16)
@@ -280,7 +282,7 @@ def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=No
     weights ``w`` [G, 2I, K].  Row r is token ``row_index[r]`` of ``a`` [T, K], or row r
     of ``a`` itself.  Returns ``h`` [M_total, I] (and ``gu``) in routed-row order."""
     M = _segments(a, offsets, w, row_index)
-    K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
+    K, inner = _gated_operands(a, sa, w, sw, experts=True)
     h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
     st = (_lib or lib()).fp8_block_grouped_gated_gemm(
         _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw),
@@ -293,7 +295,7 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
                                        scales=None, gu=None, save=False, workspace=None, stream=None):
     """The same with h leaving 1x128-quantised: ``(q, scales)``, and ``gu`` with ``save=True``."""
     M = _segments(a, offsets, w, row_index)
-    K, inner = _gated_operands(a, sa, w, sw, a.shape[0])
+    K, inner = _gated_operands(a, sa, w, sw, experts=True)
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
     scales = _scales_out(M, inner, a, scales)
     mode = _accum_code(accum, torch.bfloat16)
