@@ -123,6 +123,44 @@ def _on_gpu(*ts):
             raise ValueError("all tensors must be on the GPU")
 
 
+def _tensors(values):
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, (list, tuple)):
+            yield from _tensors(v)
+
+
+def _on_stream(stream, call, args):
+    """``call(**args)`` with ``stream`` (a torch stream or a raw handle) as the current one.
+
+    What the call allocates then comes from the memory of ``stream``: memory of the
+    stream current outside may still be in use by work queued there, which ``stream``
+    does not wait for.  Results are marked as in use on that outer stream as well."""
+    args["stream"] = None
+    for k in ("grads", "out"):  # (an iterator is gone through once)
+        if args.get(k) is not None:
+            args[k] = list(args[k])
+    given = list(_tensors(args.values()))
+    device = next((t.device for t in given if t.is_cuda), None)
+    if device is None and given:
+        return call(**args)  # raises: nothing is on the GPU
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif device is not None and stream.device != device:
+        raise ValueError("the stream must be on the tensors' GPU")
+    outer = torch.cuda.current_stream(stream.device)
+    if outer.cuda_stream == stream.cuda_stream:
+        return call(**args)
+    with torch.cuda.stream(stream):
+        result = call(**args)
+    known = {id(t) for t in given}
+    for t in _tensors(result if isinstance(result, tuple) else (result,)):
+        if id(t) not in known:
+            t.record_stream(outer)
+    return result
+
+
 def fp8_quant_act_1x128(x, q=None, scales=None, stream=None, pow2=False):
     """1x128 quantisation of the logical matrix ``x`` [M, K] along K.
 

@@ -5,6 +5,11 @@ names and the same rules as :mod:`fp8_fine_grained_amd.binding`: torch tensors
 are device memory, outputs are allocated when none are given, every step runs
 in the library's HIP kernels on torch's current stream (or ``stream=``), there
 is no fallback, and a refused call raises :class:`binding.Fp8fgError`.
+
+``stream=`` is the same as making the call with that stream current: outputs and
+scratch memory that the call allocates come from that stream's memory, and the
+outputs may be used on the stream that is current outside.  As in torch, ordering the
+two streams, and keeping the inputs until the call's work is done, is the caller's part.
 """
 
 import ctypes
@@ -14,7 +19,7 @@ from array import array
 import torch
 
 from . import binding
-from .binding import _accum_code, _check, _contig, _dtype_code, _on_gpu
+from .binding import _accum_code, _check, _contig, _dtype_code, _on_gpu, _on_stream
 
 HEADER = os.path.join(os.path.dirname(binding.HEADER), "fp8fg_layer.h")
 
@@ -57,34 +62,25 @@ def lib():
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without building the object
 
 
-def _stream(stream, t):
-    """The HIP stream of a call on tensor ``t``: ``stream``, or torch's current one."""
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+def _stream(t):
+    """torch's current HIP stream on the device of ``t``."""
+    return _raw_stream(t.get_device())
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(nbytes, given, device, stream):
-    """``given``, or ``nbytes`` of fresh scratch memory.
-
-    Fresh scratch is dropped when the call returns, before its kernels have run;
-    the allocator reuses it only after the work of the current stream, so a call
-    on another stream has to be made known to it."""
+def _workspace(nbytes, given, device):
+    """``given``, or ``nbytes`` of fresh scratch memory of the current stream (which may
+    have it back when the call returns: its next user comes after the call's kernels)."""
     if given is not None:
         _on_gpu(given)
         _contig(given)
         return given, given.numel() * given.element_size()
     if nbytes == 0:
         return None, 0
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-        ws.record_stream(s)
-    return ws, nbytes
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
 def _rows(*ts):
@@ -131,6 +127,8 @@ def fp8_add_rmsnorm_quant_1x128(x, weight, residual=None, eps=1e-6, pow2=False, 
     Pass ``y`` (of x's type) to also have the normed rows in high precision.
     Returns ``(h, q uint8 [M, H], scales fp32 [M, H/128], rstd fp32 [M])``;
     ``h`` is x + residual rounded to x's type, and x itself without a residual."""
+    if stream is not None:
+        return _on_stream(stream, fp8_add_rmsnorm_quant_1x128, locals())
     _on_gpu(x, weight, residual)
     _rows(x, residual)
     M, H = x.shape
@@ -156,7 +154,7 @@ def fp8_add_rmsnorm_quant_1x128(x, weight, residual=None, eps=1e-6, pow2=False, 
     st = (_lib or lib()).fp8_add_rmsnorm_quant_1x128(
         x.data_ptr(), _ptr(residual), _dtype_code(dt), M, H, _ld(x), _ld(residual), weight.data_ptr(),
         _dtype_code(weight.dtype), eps, 1 if pow2 else 0, _ptr(h), _ptr(y), q.data_ptr(), scales.data_ptr(),
-        rstd.data_ptr(), _stream(stream, x))
+        rstd.data_ptr(), _stream(x))
     _check("fp8_add_rmsnorm_quant_1x128", st)
     return x if h is None else h, q, scales, rstd
 
@@ -166,6 +164,8 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
 
     ``h`` and ``rstd`` as the forward call returned them; ``dh`` is the gradient
     that arrives along the residual stream.  ``need_dw=False``: dw is None."""
+    if stream is not None:
+        return _on_stream(stream, fp8_rmsnorm_backward, locals())
     _on_gpu(dy, h, rstd, weight, dh)
     _rows(dy, h, dh)
     M, H = dy.shape
@@ -183,10 +183,10 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
     L = _lib or lib()
     ws, nbytes = None, 0
     if dw is not None:
-        ws, nbytes = _workspace(L.fp8_rmsnorm_backward_workspace(M, H), workspace, dy.device, stream)
+        ws, nbytes = _workspace(L.fp8_rmsnorm_backward_workspace(M, H), workspace, dy.device)
     st = L.fp8_rmsnorm_backward(
         dy.data_ptr(), h.data_ptr(), _ptr(dh), _dtype_code(dy.dtype), M, H, _ld(dy), _ld(h), _ld(dh), rstd.data_ptr(),
-        weight.data_ptr(), _dtype_code(weight.dtype), dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, _stream(stream, dy))
+        weight.data_ptr(), _dtype_code(weight.dtype), dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, _stream(dy))
     _check("fp8_rmsnorm_backward", st)
     return dx, dw
 
@@ -235,12 +235,14 @@ def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=N
     ``w`` [2I, K] holds the gate rows, then the up rows; ``accum`` as in
     :func:`binding.fp8_block_gemm`.  With ``save=True`` (or a ``gu`` buffer) also
     g and u [M, 2I] for the backward pass: returns ``(h, gu)``, else ``h``."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_gated_gemm, locals())
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw)
     h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
     st = (_lib or lib()).fp8_block_gated_gemm(
         _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu),
-        M, inner, K, _stream(stream, a))
+        M, inner, K, _stream(a))
     _check("fp8_block_gated_gemm", st)
     return h if gu is None else (h, gu)
 
@@ -249,16 +251,18 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
                                workspace=None, stream=None):
     """The same with h leaving 1x128-quantised: ``(q uint8 [M, I], scales fp32 [M, I/128])``,
     and the bf16 ``gu`` [M, 2I] as a third with ``save=True``."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_gated_gemm_quant, locals())
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw)
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
     scales = _scales_out(M, inner, a, scales)
     mode = _accum_code(accum, torch.bfloat16)
     L = _lib or lib()
-    ws, nbytes = _workspace(L.fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device, stream)
+    ws, nbytes = _workspace(L.fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, 0), workspace, a.device)
     st = L.fp8_block_gated_gemm_quant(
         _ptr(a), _ptr(sa), _ptr(w), _ptr(sw), mode, 1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws),
-        nbytes, M, inner, K, _stream(stream, a))
+        nbytes, M, inner, K, _stream(a))
     _check("fp8_block_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
 
@@ -281,12 +285,14 @@ def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=No
     """The gated product over expert row segments ``offsets`` (device int32 [G+1]) with
     weights ``w`` [G, 2I, K].  Row r is token ``row_index[r]`` of ``a`` [T, K], or row r
     of ``a`` itself.  Returns ``h`` [M_total, I] (and ``gu``) in routed-row order."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_grouped_gated_gemm, locals())
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, experts=True)
     h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
     st = (_lib or lib()).fp8_block_grouped_gated_gemm(
         _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw),
-        _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(stream, a))
+        _accum_code(accum, h.dtype), _ptr(h), _dtype_code(h.dtype), _ptr(gu), M, inner, K, _stream(a))
     _check("fp8_block_grouped_gated_gemm", st)
     return h if gu is None else (h, gu)
 
@@ -294,6 +300,8 @@ def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=No
 def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, accum="fp8", pow2=False, q=None,
                                        scales=None, gu=None, save=False, workspace=None, stream=None):
     """The same with h leaving 1x128-quantised: ``(q, scales)``, and ``gu`` with ``save=True``."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_grouped_gated_gemm_quant, locals())
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, experts=True)
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
@@ -301,10 +309,10 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
     mode = _accum_code(accum, torch.bfloat16)
     L = _lib or lib()
     ws, nbytes = _workspace(L.fp8_block_gated_gemm_quant_workspace(mode, M, inner, K, w.shape[0]), workspace,
-                            a.device, stream)
+                            a.device)
     st = L.fp8_block_grouped_gated_gemm_quant(
         _ptr(a), _ptr(sa), a.shape[0], _ptr(row_index), _ptr(offsets), w.shape[0], _ptr(w), _ptr(sw), mode,
-        1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(stream, a))
+        1 if pow2 else 0, _ptr(q), _ptr(scales), _ptr(gu), _ptr(ws), nbytes, M, inner, K, _stream(a))
     _check("fp8_block_grouped_gated_gemm_quant", st)
     return (q, scales) if gu is None else (q, scales, gu)
 
@@ -318,6 +326,8 @@ def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_colu
     ``h_columns``  q_ht [I, M], s_ht [I, M/128]: h transposed, for the down
                    projection's weight gradient.
     A pair that is not asked for is (None, None)."""
+    if stream is not None:
+        return _on_stream(stream, fp8_gated_backward_quant, locals())
     _on_gpu(dh, gu)
     _rows(dh)
     _contig(gu)
@@ -335,7 +345,7 @@ def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_colu
     out = (*pair(rows, M, 2 * inner), *pair(columns, 2 * inner, M), *pair(h_columns, inner, M))
     st = (_lib or lib()).fp8_gated_backward_quant(
         _ptr(dh), _ptr(gu), _dtype_code(dh.dtype), M, inner, _ld(dh), 1 if pow2 else 0, *[_ptr(t) for t in out],
-        _stream(stream, dh))
+        _stream(dh))
     _check("fp8_gated_backward_quant", st)
     return out
 
@@ -351,7 +361,7 @@ def _gradients(grads):
             array("i", [codes[g.dtype] for g in grads]))
 
 
-def _grad_norm(grads, outs, max_norm, norm, workspace, stream):
+def _grad_norm(grads, outs, max_norm, norm, workspace):
     n = len(grads)
     ptrs, counts, dtypes = _gradients(grads)
     optrs = ptrs
@@ -367,21 +377,23 @@ def _grad_norm(grads, outs, max_norm, norm, workspace, stream):
         if norm.dtype != torch.float32 or norm.numel() != 1:
             raise ValueError("norm must be one fp32 value")
     L = _lib or lib()
-    ws, nbytes = _workspace(L.fp8fg_grad_norm_workspace(n), workspace, dev, stream)
+    ws, nbytes = _workspace(L.fp8fg_grad_norm_workspace(n), workspace, dev)
     host = [a.buffer_info()[0] for a in (ptrs, optrs, counts, dtypes)]  # (read during the call only)
     if outs is None:
-        st = L.fp8fg_grad_norm(host[0], host[2], host[3], n, norm.data_ptr(), _ptr(ws), nbytes, _stream(stream, norm))
+        st = L.fp8fg_grad_norm(host[0], host[2], host[3], n, norm.data_ptr(), _ptr(ws), nbytes, _stream(norm))
         _check("fp8fg_grad_norm", st)
     else:
         st = L.fp8fg_clip_grad_norm(host[0], host[1], host[2], host[3], n, max_norm, norm.data_ptr(), _ptr(ws), nbytes,
-                                    _stream(stream, norm))
+                                    _stream(norm))
         _check("fp8fg_clip_grad_norm", st)
     return norm
 
 
 def grad_norm(grads, norm=None, workspace=None, stream=None):
     """Global 2-norm over the list ``grads`` (fp32 or bf16, any lengths): an fp32 scalar on the device."""
-    return _grad_norm(list(grads), None, 0.0, norm, workspace, stream)
+    if stream is not None:
+        return _on_stream(stream, grad_norm, locals())
+    return _grad_norm(list(grads), None, 0.0, norm, workspace)
 
 
 def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
@@ -389,5 +401,7 @@ def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=
 
     In place, or into the tensors of ``out`` (same types and lengths).  Returns the
     norm before clipping, an fp32 scalar on the device: no value comes back to the host."""
+    if stream is not None:
+        return _on_stream(stream, clip_grad_norm, locals())
     grads = list(grads)
-    return _grad_norm(grads, grads if out is None else list(out), max_norm, norm, workspace, stream)
+    return _grad_norm(grads, grads if out is None else list(out), max_norm, norm, workspace)
