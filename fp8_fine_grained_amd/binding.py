@@ -2,7 +2,8 @@
 
 Argument marshalling only: these functions check tensor devices, dtypes and
 shapes, allocate outputs with torch when none are given, and pass raw device
-pointers plus torch's current HIP stream to the C ABI.  Every step of the
+pointers plus torch's current HIP stream (or, with ``stream=``, that stream made
+the current one for the call) to the C ABI.  Every step of the
 computation runs in the library's HIP kernels.  There is no fallback: if the
 library is not built, or a call fails, an exception is raised.
 """
@@ -92,12 +93,8 @@ def declared_functions():
     return re.findall(r"^(?:int|const char\*)\s+(\w+)\s*\(", text, flags=re.M)
 
 
-def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+def _stream():
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _ptr(t):
@@ -169,6 +166,8 @@ def fp8_quant_act_1x128(x, q=None, scales=None, stream=None, pow2=False):
     ``pow2=True`` calls fp8_quant_act_1x128_pow2 (power-of-two scales).
     Returns ``(q uint8 [M, K], scales fp32 [M, K/128])``.
     """
+    if stream is not None:
+        return _on_stream(stream, fp8_quant_act_1x128, locals())
     _on_gpu(x)
     M, K = x.shape
     if q is None:
@@ -178,7 +177,7 @@ def fp8_quant_act_1x128(x, q=None, scales=None, stream=None, pow2=False):
     _on_gpu(q, scales)
     fn = "fp8_quant_act_1x128_pow2" if pow2 else "fp8_quant_act_1x128"
     st = getattr(lib(), fn)(_ptr(x), _dtype_code(x.dtype), M, K, x.stride(0), x.stride(1),
-                            _ptr(q), _ptr(scales), _stream(stream))
+                            _ptr(q), _ptr(scales), _stream())
     _check(fn, st)
     return q, scales
 
@@ -186,6 +185,8 @@ def fp8_quant_act_1x128(x, q=None, scales=None, stream=None, pow2=False):
 def fp8_quant_weight_128x128(w, q=None, scales=None, stream=None, pow2=False):
     """128x128 quantisation of ``w`` [N, K].  Returns ``(q [N, K], scales [N/128, K/128])``.
     ``pow2=True`` calls fp8_quant_weight_128x128_pow2 (power-of-two scales)."""
+    if stream is not None:
+        return _on_stream(stream, fp8_quant_weight_128x128, locals())
     _on_gpu(w)
     N, K = w.shape
     if w.stride(1) != 1:
@@ -197,7 +198,7 @@ def fp8_quant_weight_128x128(w, q=None, scales=None, stream=None, pow2=False):
     _on_gpu(q, scales)
     fn = "fp8_quant_weight_128x128_pow2" if pow2 else "fp8_quant_weight_128x128"
     st = getattr(lib(), fn)(_ptr(w), _dtype_code(w.dtype), N, K, w.stride(0), _ptr(q),
-                            _ptr(scales), _stream(stream))
+                            _ptr(scales), _stream())
     _check(fn, st)
     return q, scales
 
@@ -207,6 +208,8 @@ def fp8_quant_act_weight(x, w, q_x=None, s_x=None, q_w=None, s_w=None, stream=No
     quantisation of ``w`` [N, K_w] in one launch (fp8_quant_act_weight).
     Returns ``(q_x, s_x, q_w, s_w)``, equal to fp8_quant_act_1x128(x) and
     fp8_quant_weight_128x128(w)."""
+    if stream is not None:
+        return _on_stream(stream, fp8_quant_act_weight, locals())
     _on_gpu(x, w)
     M, Kx = x.shape
     N, Kw = w.shape
@@ -220,7 +223,7 @@ def fp8_quant_act_weight(x, w, q_x=None, s_x=None, q_w=None, s_w=None, stream=No
     _on_gpu(q_x, s_x, q_w, s_w)
     st = lib().fp8_quant_act_weight(_ptr(x), _dtype_code(x.dtype), M, Kx, x.stride(0), _ptr(q_x), _ptr(s_x),
                                     _ptr(w), _dtype_code(w.dtype), N, Kw, w.stride(0), _ptr(q_w), _ptr(s_w),
-                                    1 if pow2 else 0, _stream(stream))
+                                    1 if pow2 else 0, _stream())
     _check("fp8_quant_act_weight", st)
     return q_x, s_x, q_w, s_w
 
@@ -231,6 +234,8 @@ def fp8_quant_per_tensor(x, layout="act", q=None, scales=None, stream=None):
     ``layout="act"`` fills scales [M, K/128] (the GEMM's A operand), ``"weight"``
     scales [M/128, K/128] (its B operand in block mode); every entry is the one
     scale.  Returns ``(q uint8 [M, K], scales)``."""
+    if stream is not None:
+        return _on_stream(stream, fp8_quant_per_tensor, locals())
     _on_gpu(x)
     M, K = x.shape
     if x.stride(1) != 1:
@@ -243,7 +248,7 @@ def fp8_quant_per_tensor(x, layout="act", q=None, scales=None, stream=None):
         scales = torch.empty((rows, K // 128), dtype=torch.float32, device=x.device)
     _on_gpu(q, scales)
     st = lib().fp8_quant_per_tensor(_ptr(x), _dtype_code(x.dtype), M, K, x.stride(0), _ptr(q), _ptr(scales), mode,
-                                    _stream(stream))
+                                    _stream())
     _check("fp8_quant_per_tensor", st)
     return q, scales
 
@@ -254,6 +259,8 @@ def fp8_quant_weight_128x128_dual(w, q=None, scales=None, q_t=None, scales_t=Non
     Returns ``(q [N, K], scales [N/128, K/128], q_t [K, N], scales_t [K/128, N/128])``;
     ``(q_t, scales_t)`` is the B operand of the data-gradient GEMM dX = dY W.
     ``pow2=True`` calls fp8_quant_weight_128x128_dual_pow2 (power-of-two scales)."""
+    if stream is not None:
+        return _on_stream(stream, fp8_quant_weight_128x128_dual, locals())
     _on_gpu(w)
     N, K = w.shape
     if w.stride(1) != 1:
@@ -266,7 +273,7 @@ def fp8_quant_weight_128x128_dual(w, q=None, scales=None, q_t=None, scales_t=Non
     _on_gpu(q, scales, q_t, scales_t)
     fn = "fp8_quant_weight_128x128_dual_pow2" if pow2 else "fp8_quant_weight_128x128_dual"
     st = getattr(lib(), fn)(_ptr(w), _dtype_code(w.dtype), N, K, w.stride(0), _ptr(q), _ptr(scales), _ptr(q_t),
-                            _ptr(scales_t), _stream(stream))
+                            _ptr(scales_t), _stream())
     _check(fn, st)
     return q, scales, q_t, scales_t
 
@@ -288,6 +295,8 @@ def fp8_block_gemm(a, sa, b, sb, b_scale_mode="block", accum=None, out_dtype=tor
                    y=None, stream=None):
     """Y = deq(a) deq(b)^T; ``accum`` "fp8", "exact" (default for fp32 output) or
     "scaled" (power-of-two scales applied by the matrix cores)."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_gemm, locals())
     _on_gpu(a, sa, b, sb)
     M, K = a.shape
     N = b.shape[0]
@@ -298,11 +307,11 @@ def fp8_block_gemm(a, sa, b, sb, b_scale_mode="block", accum=None, out_dtype=tor
     mode = {"block": B_BLOCK_128x128, "row": B_ROW_1x128}[b_scale_mode]
     if accum is None:  # the library's default summation for the output type
         st = lib().fp8_block_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), mode, _ptr(y), _dtype_code(y.dtype),
-                                  M, N, K, _stream(stream))
+                                  M, N, K, _stream())
         _check("fp8_block_gemm", st)
     else:
         st = lib().fp8_block_gemm_accum(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), mode, _accum_code(accum, y.dtype),
-                                        _ptr(y), _dtype_code(y.dtype), M, N, K, _stream(stream))
+                                        _ptr(y), _dtype_code(y.dtype), M, N, K, _stream())
         _check("fp8_block_gemm_accum", st)
     return y
 
@@ -310,6 +319,8 @@ def fp8_block_gemm(a, sa, b, sb, b_scale_mode="block", accum=None, out_dtype=tor
 def fp8_block_gemm_quant(a, sa, b, sb, accum="fp8", pow2=False, q=None, scales=None, stream=None):
     """Y = deq(a) deq(b)^T leaving the GEMM 1x128-quantised: returns (q uint8 [M, N],
     scales fp32 [M, N/128]); ``accum`` "fp8" or "scaled", ``pow2`` power-of-two scales."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_gemm_quant, locals())
     _on_gpu(a, sa, b, sb)
     M, K = a.shape
     N = b.shape[0]
@@ -320,7 +331,7 @@ def fp8_block_gemm_quant(a, sa, b, sb, accum="fp8", pow2=False, q=None, scales=N
     _on_gpu(q, scales)
     _contig(a, sa, b, sb, q, scales)
     st = lib().fp8_block_gemm_quant(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _accum_code(accum, torch.bfloat16),
-                                    1 if pow2 else 0, _ptr(q), _ptr(scales), M, N, K, _stream(stream))
+                                    1 if pow2 else 0, _ptr(q), _ptr(scales), M, N, K, _stream())
     _check("fp8_block_gemm_quant", st)
     return q, scales
 
@@ -328,6 +339,8 @@ def fp8_block_gemm_quant(a, sa, b, sb, accum="fp8", pow2=False, q=None, scales=N
 def fp8_block_grouped_gemm(a, sa, offsets, b, sb, accum=None, out_dtype=torch.bfloat16, y=None,
                            stream=None):
     """Grouped GEMM over expert row segments ``offsets`` (device int32 [G+1])."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_grouped_gemm, locals())
     _on_gpu(a, sa, offsets, b, sb)
     M, K = a.shape
     G, N, _ = b.shape
@@ -339,12 +352,12 @@ def fp8_block_grouped_gemm(a, sa, offsets, b, sb, accum=None, out_dtype=torch.bf
     _contig(a, sa, offsets, b, sb, y)
     if accum is None:  # the library's default summation for the output type
         st = lib().fp8_block_grouped_gemm(_ptr(a), _ptr(sa), _ptr(offsets), G, _ptr(b), _ptr(sb), _ptr(y),
-                                          _dtype_code(y.dtype), M, N, K, _stream(stream))
+                                          _dtype_code(y.dtype), M, N, K, _stream())
         _check("fp8_block_grouped_gemm", st)
     else:
         st = lib().fp8_block_grouped_gemm_accum(_ptr(a), _ptr(sa), _ptr(offsets), G, _ptr(b), _ptr(sb),
                                                 _accum_code(accum, y.dtype), _ptr(y), _dtype_code(y.dtype),
-                                                M, N, K, _stream(stream))
+                                                M, N, K, _stream())
         _check("fp8_block_grouped_gemm_accum", st)
     return y
 
@@ -353,6 +366,8 @@ def fp8_block_grouped_gemm_gather(a_tok, sa_tok, row_index, offsets, b, sb, accu
                                   out_dtype=torch.bfloat16, y=None, stream=None):
     """Grouped GEMM whose row r is token ``row_index[r]`` of ``a_tok`` [T, K]
     (``row_index`` device int32 [M_total]); Y stays in routed-row order."""
+    if stream is not None:
+        return _on_stream(stream, fp8_block_grouped_gemm_gather, locals())
     _on_gpu(a_tok, sa_tok, row_index, offsets, b, sb)
     T, K = a_tok.shape
     G, N, _ = b.shape
@@ -367,6 +382,6 @@ def fp8_block_grouped_gemm_gather(a_tok, sa_tok, row_index, offsets, b, sb, accu
     _contig(a_tok, sa_tok, row_index, offsets, b, sb, y)
     st = lib().fp8_block_grouped_gemm_gather(_ptr(a_tok), _ptr(sa_tok), T, _ptr(row_index), _ptr(offsets), G,
                                              _ptr(b), _ptr(sb), _accum_code(accum, y.dtype), _ptr(y),
-                                             _dtype_code(y.dtype), M, N, K, _stream(stream))
+                                             _dtype_code(y.dtype), M, N, K, _stream())
     _check("fp8_block_grouped_gemm_gather", st)
     return y
