@@ -11,6 +11,11 @@ namespace {
 
 constexpr int64_t kInt32Max = std::numeric_limits<int32_t>::max();
 
+// Launches of workgroups of 512 work-items (their number rounded up to a multiple of
+// 8), and of 16 work-items per group.
+constexpr int64_t kMostTiles = fp8fg::kMaxWorkItems / 512 / 8 * 8;
+constexpr int64_t kMostRowGroups = fp8fg::kMaxWorkItems / 256 * 16;
+
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int64_t elem_size(int dtype) { return dtype == FP8FG_BF16 ? 2 : 4; }
 bool valid_dtype(int d) { return d == FP8FG_F32 || d == FP8FG_BF16; }
@@ -122,7 +127,7 @@ int gated(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, 
           float* s_h, int pow2, void* gu, void* workspace, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream) {
   const int c = check_gated(a, sa, w, sw, accum, h, h_dtype, gu, M, I, K);
   if (c != FP8FG_OK) return c < 0 ? FP8FG_OK : c;
-  if (((M + 127) / 128) * (I / 128) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;  // launch grid
+  if (((M + 127) / 128) * (I / 128) > kMostTiles) return FP8FG_ERR_UNSUPPORTED;
   fp8fg::GemmArgs g = gated_args(a, sa, w, sw, accum, h, h_dtype, gu, M, I, K);
   g.y_scales = s_h;
   g.pow2 = pow2 == 1;
@@ -139,7 +144,7 @@ int grouped_gated(const uint8_t* a, const float* sa, int64_t T, const int32_t* r
   if (c < 0 || G == 0) return FP8FG_OK;
   if (T == 0 || !group_offsets || (!row_index && T != M_total)) return FP8FG_ERR_INVALID_ARG;
   if (!aligned(group_offsets, 4) || !aligned(row_index, 4)) return FP8FG_ERR_MISALIGNED;
-  if (G > kInt32Max || (M_total / 128 + G) * (I / 128) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;
+  if (G > kInt32Max || (M_total / 128 + G) * (I / 128) > kMostTiles) return FP8FG_ERR_UNSUPPORTED;
   if (T > kInt32Max || T * K >= (int64_t(1) << 32)) return FP8FG_ERR_UNSUPPORTED;  // 32-bit row offsets
   fp8fg::GemmArgs g = gated_args(a, sa, w, sw, accum, h, h_dtype, gu, M_total, I, K);
   g.offsets = group_offsets;
@@ -213,8 +218,11 @@ int fp8_gated_backward_quant(const void* dh, const void* gu, int dtype, int64_t 
   if (M == 0 || I == 0) return FP8FG_OK;
   if (!q && !q_t && !q_ht) return FP8FG_ERR_INVALID_ARG;
   if (I % 128 != 0 || ((q_t || q_ht) && M % 128 != 0)) return FP8FG_ERR_UNSUPPORTED;
-  // launch grids: one workgroup per 128 x 128 tile, or per 16 groups of a row
+  // launch grids: one workgroup of 512 work-items per 128 x 128 tile (bf16 walks over
+  // the tiles), or 16 work-items per group of a row
   if (M > kInt32Max || I > kInt32Max || M * (I / 128) > kInt32Max - 8) return FP8FG_ERR_UNSUPPORTED;
+  if (q_t || q_ht ? dtype == FP8FG_F32 && (M / 128) * (I / 128) > kMostTiles : M * (I / 128) > kMostRowGroups)
+    return FP8FG_ERR_UNSUPPORTED;
   const int c = check_rows(dh, dtype, I, ld_dh);
   if (c != FP8FG_OK) return c;
   if (!gu) return FP8FG_ERR_INVALID_ARG;

@@ -69,6 +69,9 @@ hipError_t launch_fp8_block_gemm_quant(const GemmArgs& g, bool pow2, hipStream_t
 hipError_t launch_gated_gemm(const GemmArgs& g, float* workspace, hipStream_t s);
 bool gated_quant_takes_workspace(const GemmArgs& g);
 
+// Work-items that one launch may have along x: HIP counts them in 32 bits.
+constexpr int64_t kMaxWorkItems = 0xFFFFFFFF;
+
 // Compute units of the current device (0 if it cannot be asked).
 int device_cus();
 

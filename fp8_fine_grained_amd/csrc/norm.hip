@@ -356,13 +356,31 @@ hipError_t launch_rmsnorm_quant(const NormArgs& a, hipStream_t s) {
   return with_forward_shape(a.H, [&](auto wpr, auto ch) {
     constexpr int WPR = decltype(wpr)::value, CH = decltype(ch)::value;
     constexpr int ROWS = norm_rows(WPR);
-    const dim3 grid(static_cast<unsigned>((a.M + ROWS - 1) / ROWS)), block(ROWS * WPR * 64);
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
-    if (a.bf16)
-      a.r ? go(rmsnorm_quant_kernel<true, WPR, CH, true>) : go(rmsnorm_quant_kernel<true, WPR, CH, false>);
-    else
-      a.r ? go(rmsnorm_quant_kernel<false, WPR, CH, true>) : go(rmsnorm_quant_kernel<false, WPR, CH, false>);
-    return hipGetLastError();
+    constexpr int64_t kMost = kMaxWorkItems / (ROWS * WPR * 64) * ROWS;  // rows of a launch: 2^26 or 2^23, nearly
+    const int64_t es = a.bf16 ? 2 : 4;
+    auto rows = [](auto* p, int64_t bytes) {
+      return p ? reinterpret_cast<decltype(p)>(reinterpret_cast<uintptr_t>(p) + bytes) : p;
+    };
+    for (int64_t m0 = 0; m0 < a.M; m0 += kMost) {
+      NormArgs b = a;
+      b.M = a.M - m0 < kMost ? a.M - m0 : kMost;
+      b.x = rows(a.x, m0 * a.ld_x * es);
+      b.r = rows(a.r, m0 * a.ld_r * es);
+      b.h = rows(a.h, m0 * a.H * es);
+      b.y = rows(a.y, m0 * a.H * es);
+      b.q = rows(a.q, m0 * a.H);
+      b.scales = rows(a.scales, m0 * (a.H / 128) * 4);
+      b.rstd = rows(a.rstd, m0 * 4);
+      const dim3 grid(static_cast<unsigned>((b.M + ROWS - 1) / ROWS)), block(ROWS * WPR * 64);
+      auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, b); };
+      if (a.bf16)
+        a.r ? go(rmsnorm_quant_kernel<true, WPR, CH, true>) : go(rmsnorm_quant_kernel<true, WPR, CH, false>);
+      else
+        a.r ? go(rmsnorm_quant_kernel<false, WPR, CH, true>) : go(rmsnorm_quant_kernel<false, WPR, CH, false>);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   });
 }
 

@@ -82,8 +82,9 @@ int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t H);
  * accum        FP8FG_ACCUM_FP8_MFMA, FP8FG_ACCUM_EXACT or FP8FG_ACCUM_SCALED_MFMA.
  * h            out [M, I] of `h_dtype`.
  * gu           out [M, 2I] of `h_dtype`, g then u, for the backward pass; or NULL.
- * Requires K % 128 == 0 with 128 <= K < 2^24, I % 128 == 0; a, w, h, gu 16-byte
- * aligned, scales 4-byte.  M == 0 or I == 0 is a no-op.
+ * Requires K % 128 == 0 with 128 <= K < 2^24, I % 128 == 0, at most 8388600 tiles of
+ * 128 x 128 outputs (ceil(M / 128) * I / 128; over experts (M_total / 128 + G) *
+ * I / 128); a, w, h, gu 16-byte aligned, scales 4-byte.  M == 0 or I == 0 is a no-op.
  */
 int fp8_block_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, int accum, void* h,
                          int h_dtype, void* gu, int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream);
@@ -145,8 +146,10 @@ int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_
  * dh           [M, I] of `dtype`, row pitch ld_dh >= I.
  * gu           [M, 2I] of `dtype`, as the forward call saved it.
  * Each output pair may be NULL (both of it), but not all three.
- * Requires I % 128 == 0, and M % 128 == 0 for the transposed pairs; dh, gu, q, q_t
- * and q_ht 16-byte aligned, ld_dh * sizeof(elem) % 16 == 0, scales 4-byte.
+ * Requires I % 128 == 0, and M % 128 == 0 for the transposed pairs; M * I / 128 at
+ * most 2^31 - 9, for q alone 2^28 - 16, for transposed pairs of fp32 values 2^30 -
+ * 1024; dh, gu, q, q_t and q_ht 16-byte aligned, ld_dh * sizeof(elem) % 16 == 0,
+ * scales 4-byte.
  * M == 0 or I == 0 is a no-op.
  */
 int fp8_gated_backward_quant(const void* dh, const void* gu, int dtype, int64_t M, int64_t I, int64_t ld_dh, int pow2,
