@@ -2,8 +2,11 @@
 // the host, then the launches.  Validation runs before any HIP call.
 #include "fp8fg_layer.h"
 
+#include <algorithm>
 #include <cstdint>
 #include <limits>
+#include <memory>
+#include <new>
 
 #include "launch.h"
 
@@ -240,6 +243,40 @@ int fp8_gated_backward_quant(const void* dh, const void* gu, int dtype, int64_t 
 
 namespace {
 
+// Whether an output of a clip overlaps another output, another tensor's gradient, or
+// part of its own: workgroups would then read what others have already scaled.
+int check_disjoint(const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes, int64_t n) {
+  struct Range {
+    uintptr_t begin, end;
+    bool written;
+  };
+  constexpr int64_t kFew = 128;  // kept on the stack
+  Range few[kFew];
+  std::unique_ptr<Range[]> many;
+  Range* r = few;
+  if (2 * n > kFew) {
+    many.reset(new (std::nothrow) Range[2 * n]);
+    if (!many) return FP8FG_ERR_UNSUPPORTED;
+    r = many.get();
+  }
+  int64_t k = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (counts[i] == 0) continue;
+    const uintptr_t bytes = static_cast<uintptr_t>(counts[i] * elem_size(dtypes[i]));
+    const uintptr_t in = reinterpret_cast<uintptr_t>(grads[i]), out = reinterpret_cast<uintptr_t>(outs[i]);
+    r[k++] = Range{out, out + bytes, true};
+    if (in != out) r[k++] = Range{in, in + bytes, false};
+  }
+  std::sort(r, r + k, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t read_end = 0, written_end = 0;
+  for (int64_t i = 0; i < k; ++i) {
+    if (r[i].begin < written_end || (r[i].written && r[i].begin < read_end)) return FP8FG_ERR_INVALID_ARG;
+    uintptr_t& end = r[i].written ? written_end : read_end;
+    end = std::max(end, r[i].end);
+  }
+  return FP8FG_OK;
+}
+
 int grad_norm(const void* const* grads, void* const* outs, bool clip, const int64_t* counts, const int* dtypes,
               int64_t n, float max_norm, float* norm, void* workspace, int64_t workspace_bytes,
               fp8fg_stream_t stream) {
@@ -256,6 +293,10 @@ int grad_norm(const void* const* grads, void* const* outs, bool clip, const int6
     if (counts[i] > kMostElements) return FP8FG_ERR_UNSUPPORTED;
     const unsigned es = static_cast<unsigned>(elem_size(dtypes[i]));
     if (!aligned(grads[i], es) || (clip && !aligned(outs[i], es))) return FP8FG_ERR_MISALIGNED;
+  }
+  if (clip) {
+    const int c = check_disjoint(grads, outs, counts, dtypes, n);
+    if (c != FP8FG_OK) return c;
   }
   fp8fg::GradList g{};
   g.grads = grads; g.outs = clip ? outs : nullptr; g.counts = counts; g.dtypes = dtypes; g.n = n;

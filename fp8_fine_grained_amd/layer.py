@@ -399,7 +399,8 @@ def grad_norm(grads, norm=None, workspace=None, stream=None):
 def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None, stream=None):
     """Scale every tensor of ``grads`` by min(1, max_norm / norm), norm the global 2-norm.
 
-    In place, or into the tensors of ``out`` (same types and lengths).  Returns the
+    In place, or into the tensors of ``out`` (same types and lengths).  No tensor that is
+    written may be listed twice, or overlap another of either list.  Returns the
     norm before clipping, an fp32 scalar on the device: no value comes back to the host."""
     if stream is not None:
         return _on_stream(stream, clip_grad_norm, locals())

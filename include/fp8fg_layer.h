@@ -174,7 +174,10 @@ int fp8fg_grad_norm(const void* const* grads, const int64_t* counts, const int* 
  *     c = norm <= max_norm ? 1 : max_norm / norm
  * (a norm that is not a number makes c, and so every output, not a number).
  * outs         HOST array of n device pointers, of the gradients' types and
- *              counts; outs[i] == grads[i] scales in place.
+ *              counts; outs[i] == grads[i] scales in place.  No output may
+ *              overlap another output or another gradient, or its own in part
+ *              (FP8FG_ERR_INVALID_ARG): a tensor listed twice would be scaled
+ *              while it is read.  fp8fg_grad_norm takes any list.
  * Requires max_norm > 0.  Other arguments as fp8fg_grad_norm.
  */
 int fp8fg_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes,
