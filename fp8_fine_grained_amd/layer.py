@@ -4,7 +4,8 @@ The operators between the FP8 GEMMs of a feed-forward sublayer, with the same
 names and the same rules as :mod:`fp8_fine_grained_amd.binding`: torch tensors
 are device memory, outputs are allocated when none are given, every step runs
 in the library's HIP kernels on torch's current stream (or ``stream=``), there
-is no fallback, and a refused call raises :class:`binding.Fp8fgError`.
+is no fallback, and a refused call raises :class:`binding.Fp8fgError`.  A call's
+tensors have to be on one GPU, which need not be the current one.
 
 ``stream=`` is the same as making the call with that stream current: outputs and
 scratch memory that the call allocates come from that stream's memory, and the
@@ -19,7 +20,7 @@ from array import array
 import torch
 
 from . import binding
-from .binding import _accum_code, _check, _contig, _dtype_code, _on_gpu, _on_stream
+from .binding import _accum_code, _check, _contig, _dtype_code, _on_stream
 
 HEADER = os.path.join(os.path.dirname(binding.HEADER), "fp8fg_layer.h")
 
@@ -60,11 +61,29 @@ def lib():
 # short: pointers and the stream go as plain integers, only what a caller passed
 # in is checked, and each output is one allocation.
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() without building the object
+_current_gpu = torch._C._cuda_getDevice
 
 
 def _stream(t):
     """torch's current HIP stream on the device of ``t``."""
     return _raw_stream(t.get_device())
+
+
+def _elsewhere(first, *rest):
+    """Whether the tensors (or None), which have to be on one GPU, are on another than the current one."""
+    at = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != at:
+            raise ValueError("all tensors must be on one GPU")
+    if at < 0:
+        raise ValueError("all tensors must be on one GPU")
+    return at != _current_gpu()
+
+
+def _over_there(t, call, args):
+    """``call(**args)`` with the GPU of ``t`` as the current one, whose kernels are launched."""
+    with torch.cuda.device(t.get_device()):
+        return call(**args)
 
 
 def _ptr(t):
@@ -75,7 +94,6 @@ def _workspace(nbytes, given, device):
     """``given``, or ``nbytes`` of fresh scratch memory of the current stream (which may
     have it back when the call returns: its next user comes after the call's kernels)."""
     if given is not None:
-        _on_gpu(given)
         _contig(given)
         return given, given.numel() * given.element_size()
     if nbytes == 0:
@@ -108,8 +126,6 @@ def _given(what, dtype, shape, *ts):
         if t is not None:
             if t.dtype != dtype or t.shape != shape:
                 raise ValueError(f"{what} must be {dtype} {list(shape)}")
-            if not t.is_cuda:
-                raise ValueError("all tensors must be on the GPU")
             if not t.is_contiguous():
                 raise ValueError(f"{what} must be contiguous")
 
@@ -129,7 +145,8 @@ def fp8_add_rmsnorm_quant_1x128(x, weight, residual=None, eps=1e-6, pow2=False, 
     ``h`` is x + residual rounded to x's type, and x itself without a residual."""
     if stream is not None:
         return _on_stream(stream, fp8_add_rmsnorm_quant_1x128, locals())
-    _on_gpu(x, weight, residual)
+    if _elsewhere(x, weight, residual, h, y, q, scales, rstd):
+        return _over_there(x, fp8_add_rmsnorm_quant_1x128, locals())
     _rows(x, residual)
     M, H = x.shape
     dt = x.dtype
@@ -166,7 +183,8 @@ def fp8_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dw=None, need_dw
     that arrives along the residual stream.  ``need_dw=False``: dw is None."""
     if stream is not None:
         return _on_stream(stream, fp8_rmsnorm_backward, locals())
-    _on_gpu(dy, h, rstd, weight, dh)
+    if _elsewhere(dy, h, rstd, weight, dh, dx, dw, workspace):
+        return _over_there(dy, fp8_rmsnorm_backward, locals())
     _rows(dy, h, dh)
     M, H = dy.shape
     _like("h and dh", dy.dtype, (M, H), h, dh)
@@ -237,6 +255,8 @@ def fp8_block_gated_gemm(a, sa, w, sw, accum=None, out_dtype=torch.bfloat16, h=N
     g and u [M, 2I] for the backward pass: returns ``(h, gu)``, else ``h``."""
     if stream is not None:
         return _on_stream(stream, fp8_block_gated_gemm, locals())
+    if _elsewhere(a, sa, w, sw, h, gu):
+        return _over_there(a, fp8_block_gated_gemm, locals())
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw)
     h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
@@ -253,6 +273,8 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
     and the bf16 ``gu`` [M, 2I] as a third with ``save=True``."""
     if stream is not None:
         return _on_stream(stream, fp8_block_gated_gemm_quant, locals())
+    if _elsewhere(a, sa, w, sw, q, scales, gu, workspace):
+        return _over_there(a, fp8_block_gated_gemm_quant, locals())
     M = a.shape[0]
     K, inner = _gated_operands(a, sa, w, sw)
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
@@ -270,7 +292,6 @@ def fp8_block_gated_gemm_quant(a, sa, w, sw, accum="fp8", pow2=False, q=None, sc
 def _segments(a, offsets, w, row_index):
     if w.dim() != 3 or offsets.dtype != torch.int32 or offsets.numel() != w.shape[0] + 1:
         raise ValueError("w must be [G, 2I, K] and offsets int32 [G+1]")
-    _on_gpu(offsets, row_index)
     _contig(offsets)
     if row_index is None:
         return a.shape[0]
@@ -287,6 +308,8 @@ def fp8_block_grouped_gated_gemm(a, sa, offsets, w, sw, row_index=None, accum=No
     of ``a`` itself.  Returns ``h`` [M_total, I] (and ``gu``) in routed-row order."""
     if stream is not None:
         return _on_stream(stream, fp8_block_grouped_gated_gemm, locals())
+    if _elsewhere(a, sa, offsets, w, sw, row_index, h, gu):
+        return _over_there(a, fp8_block_grouped_gated_gemm, locals())
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, experts=True)
     h, gu = _gated_outputs(M, inner, out_dtype, a, h, gu, save)
@@ -302,6 +325,8 @@ def fp8_block_grouped_gated_gemm_quant(a, sa, offsets, w, sw, row_index=None, ac
     """The same with h leaving 1x128-quantised: ``(q, scales)``, and ``gu`` with ``save=True``."""
     if stream is not None:
         return _on_stream(stream, fp8_block_grouped_gated_gemm_quant, locals())
+    if _elsewhere(a, sa, offsets, w, sw, row_index, q, scales, gu, workspace):
+        return _over_there(a, fp8_block_grouped_gated_gemm_quant, locals())
     M = _segments(a, offsets, w, row_index)
     K, inner = _gated_operands(a, sa, w, sw, experts=True)
     q, gu = _gated_outputs(M, inner, torch.uint8, a, q, gu, save)
@@ -328,7 +353,8 @@ def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_colu
     A pair that is not asked for is (None, None)."""
     if stream is not None:
         return _on_stream(stream, fp8_gated_backward_quant, locals())
-    _on_gpu(dh, gu)
+    if _elsewhere(dh, gu):
+        return _over_there(dh, fp8_gated_backward_quant, locals())
     _rows(dh)
     _contig(gu)
     M, inner = dh.shape
@@ -352,8 +378,6 @@ def fp8_gated_backward_quant(dh, gu, pow2=False, rows=True, columns=True, h_colu
 
 def _gradients(grads):
     """(device pointers, counts, type codes) of a list of gradients, as host arrays."""
-    if False in [g.is_cuda for g in grads]:
-        raise ValueError("all tensors must be on the GPU")
     if False in [g.is_contiguous() for g in grads]:
         raise ValueError("gradients and outputs must be contiguous")
     codes = {d: _dtype_code(d) for d in {g.dtype for g in grads}}
@@ -363,6 +387,10 @@ def _gradients(grads):
 
 def _grad_norm(grads, outs, max_norm, norm, workspace):
     n = len(grads)
+    tensors = [*grads, *(() if outs is None or outs is grads else outs), *(t for t in (norm, workspace) if t is not None)]
+    if tensors and _elsewhere(*tensors):
+        return _over_there(tensors[0], _grad_norm, dict(grads=grads, outs=outs, max_norm=max_norm, norm=norm,
+                                                        workspace=workspace))
     ptrs, counts, dtypes = _gradients(grads)
     optrs = ptrs
     if outs is not None and outs is not grads:
@@ -372,10 +400,8 @@ def _grad_norm(grads, outs, max_norm, norm, workspace):
     dev = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=dev)
-    else:
-        _on_gpu(norm)
-        if norm.dtype != torch.float32 or norm.numel() != 1:
-            raise ValueError("norm must be one fp32 value")
+    elif norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one fp32 value")
     L = _lib or lib()
     ws, nbytes = _workspace(L.fp8fg_grad_norm_workspace(n), workspace, dev)
     host = [a.buffer_info()[0] for a in (ptrs, optrs, counts, dtypes)]  # (read during the call only)
