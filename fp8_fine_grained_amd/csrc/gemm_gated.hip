@@ -3,8 +3,7 @@
 // in one kernel: the gate and up values stay in the accumulators, and only h
 // (bf16, fp32 or already 1x128-quantised) and, for training, the values its
 // gradient reads leave the chip.
-#include <cmath>
-
+#include "gated_shape.h"
 #include "gemm_fp8_tile.h"
 #include "lanes.h"
 
@@ -23,11 +22,7 @@ FParams gated_params(const GemmArgs& g) {
   return p;
 }
 
-// Row tiles of BM rows: exact when dense, an upper bound over segments.
-int64_t row_tiles(const GemmArgs& g, int BM) {
-  if (!g.offsets) return (g.M + BM - 1) / BM;
-  return g.M / BM + (g.G < g.M ? g.G : g.M);
-}
+int64_t row_tiles(const GemmArgs& g, int BM) { return gated_row_tiles(g.M, g.G, g.offsets != nullptr, BM); }
 
 template <int CFG, bool EXACT, bool SCALED, bool GROUPED>
 hipError_t launch_tiles(const GemmArgs& g, hipStream_t s) {
@@ -326,18 +321,6 @@ __global__ void __launch_bounds__(256) gated_quant_kernel(const float* __restric
   if (part == 0) scales[t] = s;
 }
 
-// The workgroup shapes: output columns and rows, and the time of one round of the
-// compute units, start + per_block * K/128 (us).  The last two are the tile
-// kernel's 128 x 256 and 256 x 256 tiles, the others the kernel above.
-struct Shape {
-  int cols, rows;
-  float start, per_block;
-};
-constexpr Shape kShapes[] = {{8, 16, 0.8f, 0.073f},  {16, 16, 0.5f, 0.14f}, {32, 16, 0.7f, 0.19f},
-                             {16, 32, 0.9f, 0.155f}, {32, 32, 1.8f, 0.22f}, {32, 64, 2.9f, 0.32f},
-                             {128, 128, 2.1f, 1.0f}, {128, 256, 1.9f, 1.6f}};
-constexpr int kTile128 = 6, kTile256 = 7;
-
 template <int MODE>
 hipError_t launch_mode(const GemmArgs& g, int shape, hipStream_t s) {
   switch (shape) {
@@ -359,41 +342,12 @@ hipError_t launch_mode(const GemmArgs& g, int shape, hipStream_t s) {
   }
 }
 
-// The shape of the least estimated time: rounds of the compute units times the
-// time of a round.  The times are fitted to every shape measured on 290 problems
-// (256 units; FP8 and exact sums; weights from 0.5 to 900 MB, 1 to 8192 rows, up
-// to 256 experts); the choice then costs 0.4% over the best shape of each dense FP8
-// or scaled problem on average (10% at worst) and 4% with experts, where the rows of
-// each are unknown here.  Against the tile kernel alone: one token of 2048 x 7168 7.6
-// instead of 83 us, 64 rows 13 instead of 90; against 256-row tiles alone: 777
-// rows 50 instead of 88.
-// Quantised outputs of the small tiles take a second launch, 3 us.
 int choose_shape(const GemmArgs& g, bool quantised, bool tiles_only) {
+  GatedProblem p{};
+  p.M = g.M; p.I = g.N / 2; p.K = g.K; p.G = g.G;
+  p.grouped = g.offsets != nullptr; p.exact = g.exact; p.quantised = quantised; p.tiles_only = tiles_only;
   const int found = device_cus();
-  const double cus = found > 0 ? found : 256;
-  const int64_t I = g.N / 2, KB = g.K / 128;
-  // Segments that may hold rows, and the rows of one: a quarter more than the mean,
-  // since the fuller half of the experts decides.
-  const int64_t groups = g.offsets ? (g.G < g.M ? g.G : g.M) : 1;
-  const int64_t mean = (g.M + groups - 1) / groups;
-  const int64_t rows = g.offsets ? (5 * mean + 3) / 4 : mean;
-  int best = kTile128;
-  double least = 0;
-  for (int i = tiles_only ? kTile128 : 0; i <= (g.exact || g.offsets ? kTile128 : kTile256); ++i) {
-    const Shape& t = kShapes[i];
-    // (more rows than the problem has: the time per round would go into repeated rows)
-    if (i < kTile128 && ((t.rows > 16 && t.rows >= 2 * mean) || row_tiles(g, t.rows) > 65535)) continue;
-    double per_block = t.per_block;
-    if (i == kTile128) per_block *= (g.exact ? 1.55 : 1.0) * (rows <= 64 ? 0.7 : 1.0);
-    const double wgs = static_cast<double>(groups * ((rows + t.rows - 1) / t.rows)) * ((I + t.cols - 1) / t.cols);
-    double time = std::ceil(wgs / cus) * (t.start + KB * per_block);
-    if (quantised && i < kTile128) time += 3.0;
-    if (least == 0 || time < least) {
-      least = time;
-      best = i;
-    }
-  }
-  return best;
+  return choose_gated_shape(p, found > 0 ? found : 256);
 }
 
 hipError_t launch_shape(const GemmArgs& g, int shape, hipStream_t s) {

@@ -387,7 +387,8 @@ def _gradients(grads):
 
 def _grad_norm(grads, outs, max_norm, norm, workspace):
     n = len(grads)
-    tensors = [*grads, *(() if outs is None or outs is grads else outs), *(t for t in (norm, workspace) if t is not None)]
+    tensors = [*grads, *(() if outs is None or outs is grads else outs),
+               *(t for t in (norm, workspace) if t is not None)]
     if tensors and _elsewhere(*tensors):
         return _over_there(tensors[0], _grad_norm, dict(grads=grads, outs=outs, max_norm=max_norm, norm=norm,
                                                         workspace=workspace))
