@@ -34,8 +34,10 @@ inline int64_t gated_row_tiles(int64_t M, int64_t G, bool grouped, int rows) {
 
 // The shape of the least estimated time: rounds of the compute units times the
 // time of a round.  The times are fitted to every shape's measured times on 256 units
-// (FP8 and exact sums; 1 to 8192 rows, up to 256 experts).  Against the tile kernel
-// alone: one token of 2048 x 7168 7.6 instead of 83 us, 64 rows 13 instead of 90;
+// (FP8 and exact sums; 1 to 8192 rows, up to 256 experts).  On 143 problems the choice
+// costs 0.1% over the best shape with dense operands on average (4% at worst), with
+// experts 0.1% for FP8 sums and 6% for exact ones (27% at worst: 64 experts of 4 rows).
+// Against the tile kernel alone: one token of 2048 x 7168 7.6 instead of 83 us, 64 rows 13 instead of 90;
 // against 256-row tiles alone: 777 rows 50 instead of 88.
 // Quantised outputs of the small tiles take a second launch, 3 us.
 inline int choose_gated_shape(const GatedProblem& p, double cus) {

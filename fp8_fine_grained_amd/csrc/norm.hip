@@ -322,7 +322,10 @@ __global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* __restrict
 // 8 x 2 octets take 38.8 us forward and 46.4 backward, 4 x 4 39.9 and 57.3, 16 x 1
 // 43.7 and 46.7, and one row alone takes 3.5, 4.7 and 3.1 us forward.  The backward
 // pass, which keeps dw in registers as well, stays at eight wavefronts, with 256
-// registers a lane (18432, 4096 rows: 16 x 3 spilled, 363 us).
+// registers a lane (18432, 4096 rows: 16 x 3 spilled, 363 us; 8 x 5 takes 144 bf16 and
+// 251 fp32).  Six and eight octets a lane spill (4 to 163 registers): 24576 and 32768
+// take 211 and 529 us in bf16, 426 and 809 in fp32, against 164, 218, 327 and 437 at
+// the copy rate.
 #define FP8FG_SHAPE(WPR, CH) f(std::integral_constant<int, WPR>{}, std::integral_constant<int, CH>{})
 template <typename F>
 hipError_t with_short_shape(int64_t H, F&& f) {

@@ -139,6 +139,9 @@ int fp8_block_grouped_gated_gemm_quant(const uint8_t* a, const float* sa, int64_
  *                 of it with the transposed quantisation of X.
  *     q_ht, s_ht  [I, M], [I, M/128]: h transposed, quantised along the tokens, for
  *                 the down projection's dW.
+ * The groups along the tokens start at row 0, whatever experts the rows belong to: for
+ * the weight gradients of experts, one call per expert on its rows, zero rows added
+ * to a multiple of 128.
  * Quantisation by the rule of fp8_quant_act_1x128, or of its _pow2 form; a group whose
  * largest value lies below 448 * 2^-126 (saturated gates, say) has zero codes, or with
  * pow2 codes at the smallest normal scale.
