@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfp8fg.so")
 SOURCES = ["quant.hip", "gemm.hip", "gemm_fp8.hip", "gemm_gated.hip", "gated_backward.hip", "norm.hip", "clip.hip",
-           "capi.cpp", "capi_layer.cpp"]
+           "route.hip", "segments.hip", "combine.hip", "fp4.hip", "capi.cpp", "capi_layer.cpp", "capi_experts.cpp"]
 ARCH = os.environ.get("FP8FG_ARCH", "gfx950")
 
 FLAGS = [

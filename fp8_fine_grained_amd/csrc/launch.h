@@ -137,4 +137,95 @@ constexpr int kGradBatch = 120;        // tensors per launch (kernel arguments)
 constexpr int kGradPartials = 1024;    // workgroups, hence partial sums, per launch
 hipError_t launch_grad_norm(const GradList& g, float max_norm, float* norm, double* partial, hipStream_t s);
 
+// Routing (route.hip): scores, the k chosen experts of every token and their weights.
+struct RouteArgs {
+  const void* z;        // logits [T, E], row pitch ld
+  const float* bias;    // or null
+  const uint8_t* mask;  // or null
+  int32_t* experts;
+  float* weights;
+  float* scores;  // or null
+  int64_t T, ld;
+  int E, groups, kept, terms, k;
+  float scale;
+  bool bf16, sigmoid, renormalise;
+};
+constexpr int kRouteMaxE = 1024, kRouteMaxK = 32, kRouteMaxGroups = 64;
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+
+struct RouteGradArgs {
+  const float* dw;
+  const int32_t* experts;
+  const void* z;
+  const float* ds;  // or null
+  void* dz;
+  int64_t T, ld;
+  int E, k;
+  float scale;
+  bool bf16, sigmoid, renormalise;
+};
+hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t s);
+
+// Row segments of the n = T * k chosen experts (segments.hip): a stable counting sort.
+// workspace: segments_workspace(n, G) ints.
+struct SegmentArgs {
+  const int32_t* experts;
+  int32_t* offsets;
+  int32_t* row_index;
+  int32_t* positions;
+  int32_t* counts;  // the workspace
+  int64_t n, first;
+  int k, G;
+};
+constexpr int kSegmentMaxG = 1024;
+int64_t segments_workspace(int64_t n, int64_t G);
+hipError_t launch_segments(const SegmentArgs& a, hipStream_t s);
+
+// Combination of the experts' rows and its gradient (combine.hip).
+struct CombineArgs {
+  const void* rows;
+  const int32_t* positions;
+  const float* weights;  // or null: ones
+  const void* base;      // or null
+  void* y;
+  int64_t R, H, ld_rows, ld_base, T;
+  int k;
+  bool bf16;
+};
+constexpr int kCombineMaxK = 32;
+hipError_t launch_combine(const CombineArgs& a, hipStream_t s);
+
+struct CombineGradArgs {
+  const void* dy;
+  const void* rows;  // null: no dw
+  const int32_t* positions;
+  const float* weights;  // or null: ones
+  void* drows;           // of dy's type, or codes when scales is set; or null
+  float* scales;
+  float* dw;  // or null
+  int64_t R, H, ld_dy, ld_rows, T;
+  int k;
+  bool bf16, pow2;
+};
+hipError_t launch_combine_backward(const CombineGradArgs& a, hipStream_t s);
+
+// 4-bit weights (fp4.hip): their quantisation, and products of few rows with them.
+hipError_t launch_fp4_quant(const void* w, bool bf16, int64_t N, int64_t K, int64_t ld, uint8_t* q, uint8_t* scales,
+                            hipStream_t s);
+struct Fp4Args {
+  const void* x;
+  const float* sx;  // null: x is bf16
+  const uint8_t* w;
+  const uint8_t* sw;
+  void* y;
+  const int32_t* offsets;  // grouped only
+  const int32_t* row_index;
+  int64_t M, N, K, G, T;  // N: output columns (w has 2N rows when gated)
+  bool gated, y_bf16;
+};
+hipError_t launch_fp4_gemm(const Fp4Args& a, hipStream_t s);
+// Row tiles and workgroups of a launch: the host checks that HIP can number them.
+int64_t fp4_workgroups(const Fp4Args& a);
+constexpr int64_t kFp4Threads = 512;
+
 }  // namespace fp8fg
