@@ -6,11 +6,13 @@
 #include <cstdint>
 #include <limits>
 
+#include "fp4_shape.h"
 #include "launch.h"
 
 namespace {
 
 constexpr int64_t kInt32Max = std::numeric_limits<int32_t>::max();
+constexpr int64_t kUint32Max = std::numeric_limits<uint32_t>::max();
 constexpr int64_t kInt64Max = std::numeric_limits<int64_t>::max();
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -209,8 +211,13 @@ int fp4_product(const void* x, const float* sx, int64_t T, const int32_t* row_in
     return FP8FG_ERR_UNSUPPORTED;
   if (!x || !w || !sw || !y) return FP8FG_ERR_INVALID_ARG;
   if (grouped && (T == 0 || !offsets || (!row_index && T != M))) return FP8FG_ERR_INVALID_ARG;
-  // (bytes of the weights, in 64 bits)
+  // The weights' bytes are counted in 64 bits, tiles in 31, lanes' offsets (from a tile's gate rows to its up
+  // rows, from the first token to the last) in 32.
   if (G > kInt64Max / 2 / (gated ? 2 : 1) / N / K) return FP8FG_ERR_UNSUPPORTED;
+  for (const fp8fg::Fp4Shape& s : fp8fg::kFp4Shapes)
+    if (fp8fg::fp4_tiles(M, N, G, grouped, gated, s) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;
+  if (gated && (N + 128) * (K / 2) > kUint32Max) return FP8FG_ERR_UNSUPPORTED;
+  if (grouped && row_index && T * K * (sx ? 1 : 2) > kUint32Max) return FP8FG_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
       !aligned(y, static_cast<unsigned>(elem_size(y_dtype))) || !aligned(offsets, 4) || !aligned(row_index, 4))
     return FP8FG_ERR_MISALIGNED;
@@ -220,7 +227,6 @@ int fp4_product(const void* x, const float* sx, int64_t T, const int32_t* row_in
   a.M = M; a.N = N; a.K = K; a.G = G; a.T = T;
   a.gated = gated;
   a.y_bf16 = y_dtype == FP8FG_BF16;
-  if (fp8fg::fp4_workgroups(a) > fp8fg::kMaxWorkItems / fp8fg::kFp4Threads) return FP8FG_ERR_UNSUPPORTED;
   return hip_status(fp8fg::launch_fp4_gemm(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -224,8 +224,5 @@ struct Fp4Args {
   bool gated, y_bf16;
 };
 hipError_t launch_fp4_gemm(const Fp4Args& a, hipStream_t s);
-// Row tiles and workgroups of a launch: the host checks that HIP can number them.
-int64_t fp4_workgroups(const Fp4Args& a);
-constexpr int64_t kFp4Threads = 512;
 
 }  // namespace fp8fg

@@ -169,7 +169,7 @@ int fp4_quant_weight_1x32(const void* w, int w_dtype, int64_t N, int64_t K, int6
 
 /*
  * Products of few rows with 4-bit weights:  Y = X * deq(W)^T, every product exact, summed
- * in fp32.  The weights are read once per 64 rows of X, so this is for the rows of single
+ * in fp32.  The weights are read once per 32 rows of X, so this is for the rows of single
  * tokens; any number of rows is correct.
  *
  * x, sx        sx == NULL: X is bf16 [M, K].  Else E4M3 codes [M, K] and fp32 scales
@@ -177,15 +177,17 @@ int fp4_quant_weight_1x32(const void* w, int w_dtype, int64_t N, int64_t K, int6
  * w, sw        codes [N, K/2] and scales [N, K/32] as fp4_quant_weight_1x32 writes them
  *              (scale bytes 0 and 255 give unspecified values, never a fault).
  * y            out, [M, N] of `y_dtype`.
- * Requires K % 128 == 0, 128 <= K < 2^24, M < 2^31, N < 2^31 (any N); x and w 16-byte
- * aligned, sx, sw and y 4-byte (bf16 y 2-byte).  M == 0 or N == 0 is a no-op.
+ * Requires K % 128 == 0, 128 <= K < 2^24, M < 2^31, N < 2^31 (any N), (M + 1) * (N + 8) <
+ * 2^35; x and w 16-byte aligned, sx, sw and y 4-byte (bf16 y 2-byte).  M == 0 or N == 0 is
+ * a no-op.
  */
 int fp4_gemm(const void* x, const float* sx, const uint8_t* w, const uint8_t* sw, void* y, int y_dtype, int64_t M,
              int64_t N, int64_t K, fp8fg_stream_t stream);
 
 /*
  * The gated pair h = g * sigmoid(g) * u in one kernel: w [2I, K/2] and sw [2I, K/32] hold
- * the I gate rows, then the I up rows; h [M, I] of `h_dtype`.  Otherwise as fp4_gemm.
+ * the I gate rows, then the I up rows; h [M, I] of `h_dtype`.  Requires (I + 128) * K <
+ * 2^33; otherwise as fp4_gemm.
  */
 int fp4_gated_gemm(const void* x, const float* sx, const uint8_t* w, const uint8_t* sw, void* h, int h_dtype,
                    int64_t M, int64_t I, int64_t K, fp8fg_stream_t stream);
@@ -199,7 +201,8 @@ int fp4_gated_gemm(const void* x, const float* sx, const uint8_t* w, const uint8
  *              group_offsets[G] stay as they were.
  * Offsets that decrease or pass M_total, and indices outside [0, T), are held to them:
  * unspecified rows, never an access outside the operands.
- * Requires G < 2^31 and a launch of at most 2^32 - 1 work-items; otherwise as above.
+ * Requires G < 2^31, (M_total + 2 * min(G, M_total)) * (N + 8) < 2^35, and with row_index an X of
+ * less than 4 GiB; otherwise as above.
  */
 int fp4_grouped_gemm(const void* x, const float* sx, int64_t T, const int32_t* row_index,
                      const int32_t* group_offsets, int64_t G, const uint8_t* w, const uint8_t* sw, void* y,

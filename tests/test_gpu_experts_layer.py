@@ -283,7 +283,10 @@ def test_weights_past_four_gigabytes(gpu):
     got = ex.fp4_grouped_gemm(x, offsets, q, s)
     lo = 0
     for e, n in ((0, 1), (1, 2), (G - 2, 17), (G - 1, 3)):
-        assert torch.equal(got[lo:lo + n], ex.fp4_gemm(x[lo:lo + n], q[e].clone(), s[e].clone())), e
+        # (not bit for bit those of a dense call, whose workgroups may divide K otherwise)
+        want, size = ref.fp4_product(ref.x_values(x[lo:lo + n]), ref.fp4_values(q[e], s[e]))
+        off = (got[lo:lo + n].cpu().double() - want).abs()
+        assert torch.all(off <= sum_rel(K) * size + UB * want.abs()), e
         lo += n
     del q, s
     w = torch.empty((9 * 65536 + 8, 8192), dtype=torch.bfloat16, device=gpu)  # 9.7 GB, 2.4 GB of codes

@@ -165,11 +165,42 @@ def test_gated_products(gpu, M, I, K, codes):
             assert torch.all((got - silu(g) * u).abs() <= tol + 2.0 ** -100)
 
 
+# Rows and columns that take every workgroup shape in turn (tests/test_fp4_shapes.py).
+SHAPED = [(1, 4096), (2, 7168), (1, 9600), (7, 4000), (5, 9600), (16, 4000), (13, 7168), (16, 9600), (11, 16000),
+          (31, 7168), (64, 7168)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("M,N", SHAPED)
+def test_every_workgroup_shape(gpu, M, N, codes, gated):
+    """Dense and over segments (all rows one expert's, after an empty one), with an odd number of 128s of K, fewer
+    of them than wavefronts share K, and more than the rings hold."""
+    for K in (384, 128, 2176 if N <= 7168 else 1280):
+        x, sx, w, sw = exact_operands(M, N, K, codes, seed=K)
+        sw -= 4 if gated else 0
+        y, _ = ref.fp4_product(ref.x_values(x, sx), ref.fp4_values(w, sw))
+        xs, sxs, ws, sws = on(gpu, x, sx, w, sw)
+        stack = [torch.stack([torch.full_like(t, 77), t]) for t in (ws, sws)]
+        offsets = torch.tensor([0, 0, M], dtype=torch.int32, device=gpu)
+        if gated:
+            got = ex.fp4_gated_gemm(xs, ws, sws, sx=sxs, out_dtype=F32)
+            h = silu(y[:, :N // 2]) * y[:, N // 2:]
+            assert torch.all((got.cpu().double() - h).abs() <= 10 * U * h.abs() + 2.0 ** -100), K
+            again = ex.fp4_grouped_gated_gemm(xs, offsets, *stack, sx=sxs, out_dtype=F32)
+        else:
+            got = ex.fp4_gemm(xs, ws, sws, sx=sxs, out_dtype=F32)
+            assert torch.equal(got.cpu().double(), y), K
+            again = ex.fp4_grouped_gemm(xs, offsets, *stack, sx=sxs, out_dtype=F32)
+        assert torch.equal(got, again), K
+
+
 def _segments(counts):
     return torch.tensor([0, *torch.tensor(counts).cumsum(0).tolist()], dtype=torch.int32)
 
 
-COUNTS = [[1], [0, 1, 0], [3, 0, 5, 16, 17, 0, 1], [0, 0, 40], [64, 0, 65, 2], [1] * 70, [0] * 65 + [9], [130, 1]]
+COUNTS = [[1], [0, 1, 0], [3, 0, 5, 16, 17, 0, 1], [0, 0, 40], [64, 0, 65, 2], [1] * 70, [0] * 65 + [9], [130, 1],
+          [0, 1] * 150, [0] * 600 + [3] + [0] * 300 + [1, 2], [2] * 257]
 
 
 @pytest.mark.parametrize("gated", [False, True])
