@@ -5,6 +5,8 @@
 // scale * s_j (/ the sum of the chosen s).
 // Backward, with t_j = s_j dL/ds_j through the weights and u = dscores * s:
 //     sigmoid: dz = (t + u)(1 - s),   softmax: dz = t + u - s * sum(t + u).
+#include <type_traits>
+
 #include "activation.h"
 #include "launch.h"
 #include "lanes.h"
@@ -41,25 +43,25 @@ __device__ __forceinline__ T wave_sum(T v) {
 
 // Scores of a token's logits; lanes without an expert hold -infinity.  A logit of -infinity
 // has score 0, whatever the others are.
-template <typename F>
-__device__ __forceinline__ void scores(bool sigmoidal, const float (&z)[kSteps], F (&s)[kSteps]) {
+template <typename F, int STEPS>
+__device__ __forceinline__ void scores(bool sigmoidal, const float (&z)[STEPS], F (&s)[STEPS]) {
   if (sigmoidal) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) s[i] = F(1) / (F(1) + exp(-static_cast<F>(z[i])));
+    for (int i = 0; i < STEPS; ++i) s[i] = F(1) / (F(1) + exp(-static_cast<F>(z[i])));
   } else {
     float m = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) m = fmaxf(m, z[i]);
+    for (int i = 0; i < STEPS; ++i) m = fmaxf(m, z[i]);
     m = wave_max(m);
     F sum = 0;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
       s[i] = z[i] == -__builtin_inff() ? F(0) : exp(static_cast<F>(z[i]) - static_cast<F>(m));
       sum += s[i];
     }
     sum = wave_sum(sum);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) s[i] = s[i] == F(0) ? F(0) : s[i] / sum;
+    for (int i = 0; i < STEPS; ++i) s[i] = s[i] == F(0) ? F(0) : s[i] / sum;
   }
 }
 
@@ -78,24 +80,106 @@ __device__ __forceinline__ float shares(bool sigmoidal, float z) {
   return f == 0.0f ? 0.0f : f / sum;
 }
 
-// One wavefront per token; every choice in 64 bits.
+// ---------------------------------------------------------------- choices in 64 bits
+// A token by a whole wavefront, every choice in 64 bits: what the fast kernel below leaves over, and more than 15
+// experts per token.  Rare, so its values lie in LDS (value [E]) and not in the fast kernel's registers.
 template <bool BF16>
-__global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, double* value) {
+  const int lane = threadIdx.x & 63;
+  const double out = -__builtin_inf();
+  const float outf = -__builtin_inff();
+  auto logit = [&](int e) { return element<BF16>(a.z, t * a.ld + e); };
+  double top = out, total = 0.0;
+  if (!a.sigmoid) {
+    float m = outf;
+    for (int e = lane; e < a.E; e += 64) m = fmaxf(m, logit(e));
+    top = wave_max(m);
+    for (int e = lane; e < a.E; e += 64) total += logit(e) == outf ? 0.0 : exp(static_cast<double>(logit(e)) - top);
+    total = wave_sum(total);
+  }
+  // what experts are ranked by (score: also without a bias)
+  auto rank = [&](int e, bool score) -> double {
+    const float z = logit(e), b = a.bias ? a.bias[e] : 0.0f;
+    if (z == outf || b == outf) return out;
+    double c = z;
+    if (score || a.bias) {
+      const double f = a.sigmoid ? 1.0 / (1.0 + exp(-c)) : exp(c - top);
+      c = (a.sigmoid || f == 0.0 ? f : f / total) + static_cast<double>(b);
+    }
+    return c == c ? c : kNotANumber;
+  };
+  uint64_t stay = ~uint64_t(0);
+  const int size = a.E / a.groups;
+  if (a.kept < a.groups) {
+    for (int e = lane; e < a.E; e += 64) value[e] = rank(e, a.terms == 2);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    double first = out, second = out;
+    if (lane < a.groups) {
+      for (int i = 0; i < size; ++i) {
+        const double v = value[lane * size + i];
+        second = fmax(second, fmin(first, v));
+        first = fmax(first, v);
+      }
+    }
+    const double score = a.terms == 1 ? first : second == out ? out : first + second;
+    int before = 0;  // groups that come before this lane's
+    for (int g = 0; g < a.groups; ++g) {
+      const double o = __shfl(score, g);
+      if (o > score || (o == score && g < lane)) ++before;
+    }
+    stay = __ballot(lane < a.groups && before < a.kept && score != out);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  for (int e = lane; e < a.E; e += 64) value[e] = (stay >> (e / size & 63)) & 1 ? rank(e, false) : out;
+  int mine = -1;  // lane j: the j-th expert
+  for (int j = 0; j < a.k; ++j) {
+    double best = out;
+    int at = kRouteMaxE;
+    for (int e = lane; e < a.E; e += 64) {
+      if (value[e] > best) {
+        best = value[e];
+        at = e;
+      }
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const double o = __shfl_xor(best, d);
+      const int oa = __shfl_xor(at, d);
+      if (o > best || (o == best && oa < at)) {
+        best = o;
+        at = oa;
+      }
+    }
+    if (at == kRouteMaxE) break;  // none left
+    if ((at & 63) == lane) value[at] = out;
+    if (lane == j) mine = at;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const float z = mine >= 0 ? logit(mine) : outf;
+  float w;
+  if (a.renormalise)
+    w = shares(a.sigmoid, z);
+  else
+    w = z == outf ? 0.0f : a.sigmoid ? 1.0f / (1.0f + expf(-z)) : expf(z - static_cast<float>(top)) /
+                                                                      static_cast<float>(total);
+  if (lane < a.k) {
+    a.experts[t * a.k + lane] = mine;
+    a.weights[t * a.k + lane] = mine < 0 ? 0.0f : a.scale * w;
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kWaves * 64) route_wide_kernel(RouteArgs a) {
   __shared__ double value[kWaves][kRouteMaxE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const float out = -__builtin_inff();
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + wave; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * kWaves) {
-    float z[kSteps], s[kSteps];
-    double key[kSteps], wide[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int e = lane + 64 * i;
-      z[i] = e < a.E ? element<BF16>(a.z, t * a.ld + e) : out;
-    }
-    scores(a.sigmoid, z, s);
-    scores(a.sigmoid, z, wide);
     if (a.scores) {
+      float z[kSteps], s[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        z[i] = lane + 64 * i < a.E ? element<BF16>(a.z, t * a.ld + lane + 64 * i) : -__builtin_inff();
+      scores<float, kSteps>(a.sigmoid, z, s);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
         if (lane + 64 * i < a.E) a.scores[t * a.E + lane + 64 * i] = s[i];
@@ -107,93 +191,295 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       }
       continue;
     }
-    // what experts are ranked by, and what group scores are made of
+    route_token<BF16>(a, t, value[wave]);
+  }
+}
+
+// ---------------------------------------------------------------- the fast kernel
+// Reductions over aligned groups of L = 16 or 64 lanes.
+template <int L>
+__device__ __forceinline__ float max_of(float v) {
+  v = max16(v);
+  if constexpr (L == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float sum_of(float v) {
+  if constexpr (L == 64) return sum64(v);
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  return v + dpp<0x140>(v);
+}
+
+// The two largest of a set, of which v, or another part's two largest f and s, are met.
+__device__ __forceinline__ void merge_one(float& first, float& second, float v) {
+  second = fmaxf(second, fminf(first, v));
+  first = fmaxf(first, v);
+}
+__device__ __forceinline__ void merge_two(float& first, float& second, float f, float s) {
+  second = fmaxf(fminf(first, f), fmaxf(second, s));
+  first = fmaxf(first, f);
+}
+
+// L lanes per token, V consecutive experts per lane (so that the lowest index is the first lane's first).  Choices go
+// through fp32 keys whose low bits say where they come from: one maximum over the lane's registers and the token's
+// lanes finds an expert, and one comparison per register takes it out.
+//  * bf16 logits without a bias leave room for the whole index: the keys are exact, ties and all;
+//  * other keys give up four bits for the place in the lane.  Neighbours that lie closer than those bits and the
+//    rounding of a score are put in order by their 64-bit values.  Where that does not do (three in one place at the
+//    border, groups that lie close, softmax with a bias) the token is done again in 64 bits, and so is one with a
+//    value that is not a number or +infinity.
+// Bound by the instructions of the k rounds, not by the logits' bytes; four tokens share a wavefront because a round
+// costs the same for one (8192 x 256 in 8 groups: a wavefront per token, all in 64 bits, took 130 us).
+template <bool BF16, bool BIAS, int L, int V>
+__global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
+  constexpr bool EXACT = BF16 && !BIAS;
+  constexpr int TOKENS = 64 / L;
+  constexpr float kInf = __builtin_inff();
+  __shared__ double wide[kWaves][L * V];             // of tokens that are done again
+  __shared__ float narrow[kWaves][TOKENS][L * V];    // choices, where groups lie across lanes
+  __shared__ float group_score[kWaves][TOKENS][kRouteMaxGroups];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l = lane & (L - 1), slot = lane / L;
+  const int e0 = l * V;
+  auto of_token = [&](uint64_t ballot) -> uint64_t { return L == 64 ? ballot : (ballot >> (slot * L)) & 0xFFFF; };
+  float bias[BIAS ? V : 1];
+  if constexpr (BIAS) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int e = lane + 64 * i;
-      const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
-      const bool gone = z[i] == out || b == out;
-      const double c = wide[i] + static_cast<double>(b);
-      auto rank = [&](double v) { return gone ? static_cast<double>(out) : v == v ? v : kNotANumber; };
-      key[i] = rank(a.bias ? c : static_cast<double>(z[i]));
-      wide[i] = a.bias || a.terms == 2 ? rank(c) : key[i];
-    }
-    if (a.kept < a.groups) {
+    for (int i = 0; i < V; ++i) bias[i] = e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
+  }
+  const int size = a.E / a.groups, lanes = size / V;
+  const bool grouped = a.kept < a.groups;
+  const bool sums = grouped && a.terms == 2;  // sums of two scores are compared
+  const bool whole = size % V == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 16;  // a group is 1, 2, 4, .. lanes
+  const bool scored = BIAS || sums || a.scores || (!a.sigmoid && !a.renormalise);
+  constexpr int VEC = BF16 ? 8 : 4;  // elements of a 16-byte load
+  const bool vector = V % VEC == 0 && a.E % VEC == 0 && (a.ld * (BF16 ? 2 : 4)) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWaves * TOKENS;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * TOKENS; t0 < a.T; t0 += stride) {
+    const bool live = t0 + slot < a.T;
+    const int64_t t = live ? t0 + slot : a.T - 1;  // past the end: the last token again, not stored
+    float z[V];
+    if (vector) {
+      if constexpr (V % VEC == 0) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        if (lane + 64 * i < a.E) value[wave][lane + 64 * i] = wide[i];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const int size = a.E / a.groups;
-      double first = out, second = out;
-      if (lane < a.groups) {
-        for (int i = 0; i < size; ++i) {
-          const double v = value[wave][lane * size + i];
-          if (v > first) {
-            second = first;
-            first = v;
-          } else if (v > second) {
-            second = v;
+        for (int q = 0; q < V / VEC; ++q) {
+          const int e = e0 + q * VEC < a.E ? e0 + q * VEC : 0;
+          const u32x4 u =
+              *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.z) + (t * a.ld + e) * (BF16 ? 2 : 4));
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            uint32_t v = BF16 ? (i % 2 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16) : u[i % 4];
+            z[q * VEC + i] = e0 + q * VEC < a.E ? __uint_as_float(v) : -kInf;
           }
         }
       }
-      const double score = a.terms == 1 ? first : second == out ? static_cast<double>(out) : first + second;
-      int before = 0;  // groups that come before this lane's
-      for (int g = 0; g < a.groups; ++g) {
-        const double o = __shfl(score, g);
-        if (o > score || (o == score && g < lane)) ++before;
-      }
-      const uint64_t stay = __ballot(lane < a.groups && before < a.kept && score != out);
+    } else {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int e = lane + 64 * i;
-        if (e < a.E && !((stay >> (e / size)) & 1)) key[i] = out;
+      for (int i = 0; i < V; ++i) z[i] = e0 + i < a.E ? element<BF16>(a.z, t * a.ld + e0 + i) : -kInf;
+    }
+    float s[V], top = 0.0f, total = 1.0f, largest = 1.0f;
+    if (scored) {
+      if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float v = z[i] == z[i] ? sigmoid(z[i]) : z[i];
+          s[i] = z[i] == -kInf ? 0.0f : v;
+        }
+      } else {
+        top = -kInf;
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, z[i]);
+        top = max_of<L>(top);
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          s[i] = z[i] == -kInf ? 0.0f : expf(z[i] - top);
+          total += s[i];
+        }
+        total = sum_of<L>(total);
+        largest = 1.0f / total;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = s[i] == 0.0f ? 0.0f : s[i] * largest;
+      }
+      if (a.scores && live) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (e0 + i < a.E) a.scores[t * a.E + e0 + i] = s[i];
+      }
+    }
+    // how far an fp32 score may be off: the sigmoid's roundings; or exponential, argument, sum and quotient
+    const float off = a.sigmoid ? 0x1p-23f : 0x1p-18f * largest;
+    bool again = false;
+    float key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = BIAS ? s[i] + bias[i] : z[i] + 0.0f;  // (no -0: it equals 0)
+      if (BIAS && z[i] == -kInf) key[i] = -kInf;
+      again |= !(key[i] < kInf);  // not a number, or +infinity
+    }
+    if (grouped) {
+      // the two largest choices of every group
+      auto choice = [&](int i) { return BIAS || !sums || key[i] == -kInf ? key[i] : s[i]; };
+      float* score = group_score[wave][slot];
+      if (whole) {
+        float first = -kInf, second = -kInf;
+#pragma unroll
+        for (int i = 0; i < V; ++i) merge_one(first, second, choice(i));
+        if (lanes >= 2) merge_two(first, second, dpp<0xB1>(first), dpp<0xB1>(second));
+        if (lanes >= 4) merge_two(first, second, dpp<0x4E>(first), dpp<0x4E>(second));
+        if (lanes >= 8) merge_two(first, second, dpp<0x141>(first), dpp<0x141>(second));
+        if (lanes >= 16) merge_two(first, second, dpp<0x140>(first), dpp<0x140>(second));
+        if ((l & (lanes - 1)) == 0 && e0 < a.E)
+          score[e0 / size] = !sums ? first : second == -kInf ? -kInf : first + second;
+      } else {
+        float* c = narrow[wave][slot];
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[e0 + i] = choice(i);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int g = l; g < a.groups; g += L) {
+          float first = -kInf, second = -kInf;
+          int at = g % size;  // (groups start at different banks)
+          for (int i = 0; i < size; ++i) {
+            merge_one(first, second, c[g * size + at]);
+            at = at + 1 == size ? 0 : at + 1;
+          }
+          score[g] = !sums ? first : second == -kInf ? -kInf : first + second;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // groups with fewer than `kept` larger ones stay; the smallest that stays and the largest that does not have to
+      // be told apart (equal ones are left to the 64-bit form)
+      uint64_t stay = 0;
+      float low = kInf, high = -kInf;
+      for (int g0 = 0; g0 < a.groups; g0 += L) {
+        const int g = g0 + l;
+        const float mine = g < a.groups ? score[g] : -kInf;
+        int before = 0;
+        for (int o = 0; o < a.groups; ++o) before += score[o] > mine ? 1 : 0;
+        const bool keep = mine > -kInf && before < a.kept;
+        stay |= of_token(__ballot(keep)) << g0;
+        if (keep)
+          low = fminf(low, mine);
+        else
+          high = fmaxf(high, mine);
+      }
+      low = -max_of<L>(-low);
+      high = max_of<L>(high);
+      const float apart = BIAS || sums ? 4.0f * off + 0x1p-22f * fmaxf(fabsf(low), fabsf(high)) : 0.0f;
+      again |= (high > -kInf && !(low - high > apart)) || __popcll(stay) > a.kept;
+      int g = e0 / size, next = (g + 1) * size;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (e0 + i == next) {
+          ++g;
+          next += size;
+        }
+        if (!((stay >> (g & 63)) & 1)) key[i] = -kInf;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    int mine = -1;  // lane j: the j-th expert, its score (or its logit, for the shares)
-    float chosen = a.renormalise ? out : 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      double best = out;
-      int at = kRouteMaxE;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        if (key[i] > best) {
-          best = key[i];
-          at = lane + 64 * i;
-        }
-      }
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) {
-        const double o = __shfl_xor(best, d);
-        const int oa = __shfl_xor(at, d);
-        if (o > best || (o == best && oa < at)) {
-          best = o;
-          at = oa;
-        }
-      }
-      if (at == kRouteMaxE) break;  // none left
-      float v = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        if (at == lane + 64 * i) {
-          v = a.renormalise ? z[i] : s[i];
-          key[i] = out;
-        }
-      }
-      v = __shfl(v, at & 63);
-      if (lane == j) {
-        mine = at;
-        chosen = v;
-      }
+    for (int i = 0; i < V; ++i) {
+      uint32_t b = __float_as_uint(key[i]);
+      if constexpr (EXACT)  // (a larger low part is a smaller negative number)
+        b |= static_cast<int32_t>(b) < 0 ? static_cast<uint32_t>(e0 + i) : 1023u - (e0 + i);
+      else
+        b = (b & ~15u) | static_cast<uint32_t>(i);
+      key[i] = key[i] == -kInf ? -kInf : __uint_as_float(b);
     }
-    const float w = a.renormalise ? shares(a.sigmoid, chosen) : chosen;
-    if (lane < a.k) {
-      a.experts[t * a.k + lane] = mine;
-      a.weights[t * a.k + lane] = mine < 0 ? 0.0f : a.scale * w;
+    // Lane j: the j-th expert; of inexact keys one more than asked for, which may yet change places with the last.
+    const int found = EXACT ? a.k : a.k + 1;
+    int mine = -1;
+    float before = kInf, last = kInf;  // the key before, the last that is asked for
+    bool close = false;
+    for (int j = 0;; ++j) {
+      float best = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = fmaxf(best, key[i]);
+      const float m = max_of<L>(best);
+      if constexpr (!EXACT) {
+        const float apart = (BIAS ? 2.0f * off : 0.0f) + 0x1p-17f * fmaxf(fabsf(before), fabsf(m));
+        if (j < found) close |= j > 0 && m > -kInf && !(before - m > apart);
+        if (j == a.k - 1) last = m;
+        if (j == found) again |= m > -kInf && !(last - m > apart);  // three of a kind at the border
+      }
+      if (j == found) break;
+      const uint32_t b = __float_as_uint(m);
+      int e;
+      float gone = m;
+      if constexpr (EXACT) {
+        e = static_cast<int>(b & 1023u);
+        e = static_cast<int32_t>(b) < 0 ? e : 1023 - e;
+      } else {
+        const int from = __ffsll(static_cast<unsigned long long>(of_token(__ballot(best == m)))) - 1;
+        e = from * V + static_cast<int>(b & 15u);
+        gone = l == from ? m : kInf;  // (another lane may hold an equal key)
+      }
+      if (l == j) mine = m == -kInf ? -1 : e;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = key[i] == gone ? -kInf : key[i];
+      before = m;
+    }
+    if constexpr (!EXACT) {
+      // Neighbours that the keys cannot tell apart, found in any order: in the order of the logits themselves, or of
+      // 64-bit sums (of softmax scores the whole token's: done again).
+      if (BIAS && !a.sigmoid) {
+        again |= close;
+        close = false;
+      }
+      if (__ballot(close)) {
+        double c = -__builtin_inf();
+        if (mine >= 0) {
+          c = static_cast<double>(element<BF16>(a.z, t * a.ld + mine));
+          if constexpr (BIAS) c = 1.0 / (1.0 + exp(-c)) + static_cast<double>(a.bias[mine]);
+        }
+        int place = 0;
+        for (int o = 0; o < found; ++o) {
+          const int from = slot * L + o, eo = __shfl(mine, from);
+          const double co = __shfl(c, from);
+          if (co > c || (co == c && eo >= 0 && eo < mine)) ++place;
+        }
+        int sorted = -1;
+        for (int o = 0; o < found; ++o) {
+          const int from = slot * L + o, eo = __shfl(mine, from), po = __shfl(place, from);
+          if (po == l && eo >= 0) sorted = eo;
+        }
+        if (close) mine = sorted;
+      }
+      if (l >= a.k) mine = -1;
+    }
+    const bool masked = a.mask && a.mask[t] == 0;
+    if (masked) mine = -1;
+    const uint64_t redo = __ballot(again && live && !masked);
+    // the chosen logits again (from the caches), and their weights
+    const float zc = mine >= 0 ? element<BF16>(a.z, t * a.ld + mine) : -kInf;
+    float w;
+    if (a.renormalise) {
+      w = share(a.sigmoid, zc, max_of<L>(zc));
+      const float sum = sum_of<L>(w);
+      w = w == 0.0f ? 0.0f : w / sum;
+    } else {
+      w = mine < 0 ? 0.0f : a.sigmoid ? sigmoid(zc) : expf(zc - top) / total;
+    }
+    if (live && l < a.k && of_token(redo) == 0) {
+      a.experts[t * a.k + l] = mine;
+      a.weights[t * a.k + l] = mine < 0 ? 0.0f : a.scale * w;
+    }
+    if (redo) {
+#pragma unroll 1
+      for (int q = 0; q < TOKENS; ++q)
+        if (L == 64 || ((redo >> (q * L)) & 0xFFFF)) route_token<BF16>(a, t0 + q, wide[wave]);
     }
   }
 }
 
+// ---------------------------------------------------------------- gradient
 // One wavefront per token; lane j holds the j-th chosen expert's t.
 template <bool BF16>
 __global__ void __launch_bounds__(kWaves * 64) route_backward_kernel(RouteGradArgs a) {
@@ -207,7 +493,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_backward_kernel(RouteGradAr
       const int e = lane + 64 * i;
       z[i] = e < a.E ? element<BF16>(a.z, t * a.ld + e) : out;
     }
-    scores(a.sigmoid, z, s);
+    scores<float, kSteps>(a.sigmoid, z, s);
     int mine = lane < a.k ? a.experts[t * a.k + lane] : -1;
     if (mine >= a.E) mine = -1;
     const float dw = mine >= 0 ? a.scale * a.dw[t * a.k + lane] : 0.0f;
@@ -270,11 +556,30 @@ dim3 token_blocks(int64_t T) {
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  if (a.bf16)
-    hipLaunchKernelGGL(route_kernel<true>, token_blocks(a.T), dim3(kWaves * 64), 0, s, a);
-  else
-    hipLaunchKernelGGL(route_kernel<false>, token_blocks(a.T), dim3(kWaves * 64), 0, s, a);
-  return hipGetLastError();
+  if (a.k > 15) {
+    if (a.bf16)
+      hipLaunchKernelGGL(route_wide_kernel<true>, token_blocks(a.T), dim3(kWaves * 64), 0, s, a);
+    else
+      hipLaunchKernelGGL(route_wide_kernel<false>, token_blocks(a.T), dim3(kWaves * 64), 0, s, a);
+    return hipGetLastError();
+  }
+  auto shape = [&](auto bf16, auto bias) {
+    constexpr bool BF16 = decltype(bf16)::value, BIAS = decltype(bias)::value;
+    const dim3 narrow = token_blocks((a.T + 3) / 4), full = token_blocks(a.T), block(kWaves * 64);
+    if (a.E <= 64)
+      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 16, 4>), narrow, block, 0, s, a);
+    else if (a.E <= 128)
+      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 16, 8>), narrow, block, 0, s, a);
+    else if (a.E <= 256)
+      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 16, 16>), narrow, block, 0, s, a);
+    else if (a.E <= 512)
+      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 64, 8>), full, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 64, 16>), full, block, 0, s, a);
+    return hipGetLastError();
+  };
+  if (a.bf16) return a.bias ? shape(std::true_type{}, std::true_type{}) : shape(std::true_type{}, std::false_type{});
+  return a.bias ? shape(std::false_type{}, std::true_type{}) : shape(std::false_type{}, std::false_type{});
 }
 
 hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t s) {

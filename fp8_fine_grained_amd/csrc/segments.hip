@@ -1,108 +1,178 @@
 // Row segments of chosen experts: a stable counting sort of n entries by expert.
 //
-// A unit of the sort is one wavefront's run of consecutive entries.  The first pass counts
-// every unit's entries per expert; the second sums those counts over the units (all of them
-// for the segments' starts, the earlier ones for the unit's own), and each unit then places
-// its entries in order, 64 at a time: an entry's place among the 64 is the number of earlier
-// lanes with the same expert, found by ballots over the bits of the expert's number.  No
-// atomics between wavefronts, so the order is the entries' own.
+// A workgroup takes a run of consecutive entries, each of its wavefronts a part of it, 64
+// entries at a time.  An entry's place among the 64 is the number of earlier lanes with the
+// same expert, found by ballots over the bits of the expert's number; counts per wavefront
+// and expert are kept in LDS, and each wavefront's start in a segment is the sum of the
+// counts before it.  No atomics between wavefronts, so the order is the entries' own.
+// With more entries than one workgroup takes, a first launch counts every workgroup's
+// entries per expert, and each workgroup of the second sums the table (all of it for the
+// segments' starts, the rows before its own for its own).
 // Entries of no local expert form a last bin of their own behind the segments.
+#include <type_traits>
+
 #include "launch.h"
 
 namespace fp8fg {
 namespace {
 
-constexpr int kUnitWaves = 4;                        // units of a workgroup
-constexpr int64_t kUnit = 512;                       // entries of a unit
-constexpr int64_t kMostUnits = 1024;                 // (longer inputs take longer units)
+constexpr int kFewWaves = 4, kFewRounds = 4;      // 1024 entries: the workgroups of many, or a single small one
+constexpr int kManyWaves = 16, kManyRounds = 8;   // 8192 entries: the most of a single workgroup
+constexpr int64_t kFewRun = kFewWaves * kFewRounds * 64, kManyRun = kManyWaves * kManyRounds * 64;
+constexpr int64_t kMostGroups = 1024;             // (longer inputs: longer runs)
 
-int64_t unit_length(int64_t n) {
-  const int64_t u = (n + kMostUnits - 1) / kMostUnits;
-  return u <= kUnit ? kUnit : (u + 63) / 64 * 64;
-}
+// Entries of a workgroup when there are several.
+int64_t run_length(int64_t n) { return ((n + kMostGroups - 1) / kMostGroups + kFewRun - 1) / kFewRun * kFewRun; }
 
-__device__ __forceinline__ int bin_of(const SegmentArgs& a, int64_t i) {
-  const int64_t e = static_cast<int64_t>(a.experts[i]) - a.first;
-  return e >= 0 && e < a.G ? static_cast<int>(e) : a.G;
+// A wavefront's entries begin + 64 r + lane of r = 0 .. R - 1: their bins (-1 past `end`), all loaded together.
+template <int R>
+__device__ __forceinline__ void load_bins(const SegmentArgs& a, int64_t begin, int64_t end, int (&bin)[R]) {
+  const int lane = threadIdx.x & 63;
+  int32_t e[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = begin + 64 * r + lane;
+    e[r] = a.experts[i < end ? i : end - 1];
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t g = static_cast<int64_t>(e[r]) - a.first;
+    bin[r] = g >= 0 && g < a.G ? static_cast<int>(g) : a.G;
+    if (begin + 64 * r + lane >= end) bin[r] = -1;
+  }
 }
-// Lanes of the wavefront with the same bin (0 for a lane that takes no part).
-__device__ __forceinline__ uint64_t same_bin(int bin, bool live, int bits) {
-  uint64_t m = __ballot(live);
+// Lanes of the wavefront with the same bin (0 for a lane without an entry).
+__device__ __forceinline__ uint64_t same_bin(int bin, int bits) {
+  uint64_t m = __ballot(bin >= 0);
   for (int b = 0; b < bits; ++b) {
     const uint64_t v = __ballot((bin >> b) & 1);
     m &= (bin >> b) & 1 ? v : ~v;
   }
-  return live ? m : 0;
+  return bin >= 0 ? m : 0;
 }
+// Lanes before this one in m.
+__device__ __forceinline__ int rank_in(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), 0));
+}
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// counts[unit][bin]
-__global__ void __launch_bounds__(kUnitWaves * 64) count_kernel(SegmentArgs a, int64_t unit, int bits) {
-  __shared__ int32_t c[kUnitWaves][kSegmentMaxG + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kUnitWaves + wave;
-  for (int g = lane; g <= a.G; g += 64) c[wave][g] = 0;
-  __syncthreads();
-  const int64_t begin = u * unit, end = begin + unit < a.n ? begin + unit : a.n;
-  for (int64_t i = begin + lane; i - lane < end; i += 64) {
-    const bool live = i < end;
-    const int bin = live ? bin_of(a, i) : 0;
-    const uint64_t m = same_bin(bin, live, bits);
-    if (live && __ffsll(static_cast<unsigned long long>(m)) - 1 == lane) c[wave][bin] += __popcll(m);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+// Adds a wavefront's entries to its counts.
+template <int R>
+__device__ __forceinline__ void count(const int (&bin)[R], int bits, int32_t* c) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint64_t m = same_bin(bin[r], bits);
+    if (m != 0 && rank_in(m) == 0) c[bin[r]] += __popcll(m);
+    wave_fence();
   }
-  if (begin < a.n)
-    for (int g = lane; g <= a.G; g += 64) a.counts[u * (a.G + 1) + g] = c[wave][g];
 }
 
-__global__ void __launch_bounds__(kUnitWaves * 64) place_kernel(SegmentArgs a, int64_t unit, int bits) {
-  __shared__ int32_t at[kUnitWaves][kSegmentMaxG + 1];  // where the unit's next entry of a bin goes
+// counts[workgroup][bin]
+__global__ void __launch_bounds__(kFewWaves * 64) count_kernel(SegmentArgs a, int64_t run, int bits) {
+  __shared__ int32_t c[kFewWaves][kSegmentMaxG + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t part = run / kFewWaves;
+  const int64_t begin = blockIdx.x * run + wave * part, end = begin + part < a.n ? begin + part : a.n;
+  for (int g = lane; g <= a.G; g += 64) c[wave][g] = 0;
+  wave_fence();
+  for (int64_t i = begin; i < end; i += kFewRounds * 64) {
+    int bin[kFewRounds];
+    load_bins(a, i, end, bin);
+    count(bin, bits, c[wave]);
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g <= a.G; g += kFewWaves * 64) {
+    int32_t v = 0;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) v += c[w][g];
+    a.counts[blockIdx.x * (a.G + 1) + g] = v;
+  }
+}
+
+// WAVES wavefronts with R rounds at a time; ONE: a single workgroup, without the table.
+template <int WAVES, int R, bool ONE>
+__global__ void __launch_bounds__(WAVES * 64) place_kernel(SegmentArgs a, int64_t run, int bits) {
+  __shared__ int32_t at[WAVES][kSegmentMaxG + 1];  // counts, then where the wavefront's next entry of a bin goes
   __shared__ int32_t start[kSegmentMaxG + 1];
+  __shared__ int32_t chunk[(kSegmentMaxG + 64) / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int bins = a.G + 1;
-  const int64_t units = (a.n + unit - 1) / unit;
-  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kUnitWaves;
-  for (int g = threadIdx.x; g < bins; g += kUnitWaves * 64) {
-    int32_t total = 0;
-    for (int64_t u = 0; u < units; ++u) {
-      if (u >= u0 && u < u0 + kUnitWaves) at[u - u0][g] = total;
-      total += a.counts[u * bins + g];
-    }
-    start[g] = total;
+  const int64_t part = run / WAVES;
+  const int64_t begin = blockIdx.x * run + wave * part, end = begin + part < a.n ? begin + part : a.n;
+  for (int g = lane; g < bins; g += 64) at[wave][g] = 0;
+  wave_fence();
+  for (int64_t i = begin; i < end; i += R * 64) {
+    int bin[R];
+    load_bins(a, i, end, bin);
+    count(bin, bits, at[wave]);
   }
   __syncthreads();
-  if (wave == 0) {  // exclusive sums of the bins' totals
-    int32_t before = 0;
-    for (int g0 = 0; g0 < bins; g0 += 64) {
-      const int g = g0 + lane;
-      const int32_t v = g < bins ? start[g] : 0;
-      int32_t incl = v;
+  for (int g = threadIdx.x; g < bins; g += WAVES * 64) {
+    int32_t before = 0, total = 0;
+    if constexpr (!ONE) {
+      const int groups = gridDim.x, mine = blockIdx.x;
+      for (int b0 = 0; b0 < groups; b0 += 32) {  // 32 loads in flight
+        int32_t v[32];
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int32_t o = __shfl_up(incl, d);
-        if (lane >= d) incl += o;
+        for (int q = 0; q < 32; ++q) v[q] = a.counts[static_cast<int64_t>(b0 + q < groups ? b0 + q : 0) * bins + g];
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          const int32_t c = b0 + q < groups ? v[q] : 0;
+          total += c;
+          before += b0 + q < mine ? c : 0;
+        }
       }
-      if (g < bins) {
-        start[g] = before + incl - v;
-        if (blockIdx.x == 0) a.offsets[g] = before + incl - v;
-      }
-      before += __shfl(incl, 63);
     }
+    // the wavefronts' counts become the counts before them
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const int32_t c = at[w][g];
+      at[w][g] = before;
+      before += c;
+    }
+    start[g] = ONE ? before : total;
   }
   __syncthreads();
-  const int64_t begin = (u0 + wave) * unit, end = begin + unit < a.n ? begin + unit : a.n;
-  for (int64_t i = begin + lane; i - lane < end; i += 64) {
-    const bool live = i < end;
-    const int bin = live ? bin_of(a, i) : 0;
-    const uint64_t m = same_bin(bin, live, bits);
-    const int rank = __popcll(m & ((uint64_t(1) << lane) - 1));
-    if (live) {
-      const int32_t p = start[bin] + at[wave][bin] + rank;
-      a.positions[i] = bin < a.G ? p : -1;
-      a.row_index[p] = bin < a.G ? static_cast<int32_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.k)) : 0;
+  // exclusive sums of the bins' totals, a chunk of 64 per wavefront, then over the chunks
+  for (int g0 = wave * 64; g0 < bins; g0 += WAVES * 64) {
+    const int g = g0 + lane;
+    const int32_t v = g < bins ? start[g] : 0;
+    int32_t incl = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(incl, d);
+      if (lane >= d) incl += o;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (live && rank == 0) at[wave][bin] += __popcll(m);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (g < bins) start[g] = incl - v;
+    if (lane == 63) chunk[g0 / 64] = incl;
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < bins; g += WAVES * 64) {
+    int32_t v = start[g];
+    for (int c = 0; c < g / 64; ++c) v += chunk[c];
+    if (blockIdx.x == 0) a.offsets[g] = v;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) at[w][g] += v;
+  }
+  __syncthreads();
+  for (int64_t i = begin; i < end; i += R * 64) {
+    int bin[R];
+    load_bins(a, i, end, bin);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t m = same_bin(bin[r], bits);
+      const int rank = rank_in(m);
+      const int64_t k = i + 64 * r + lane;
+      if (m != 0) {
+        const int32_t p = at[wave][bin[r]] + rank;
+        a.positions[k] = bin[r] < a.G ? p : -1;
+        a.row_index[p] = bin[r] < a.G ? static_cast<int32_t>(static_cast<uint32_t>(k) / static_cast<uint32_t>(a.k)) : 0;
+      }
+      wave_fence();
+      if (m != 0 && rank == 0) at[wave][bin[r]] += __popcll(m);
+      wave_fence();
+    }
   }
 }
 
@@ -113,8 +183,9 @@ __global__ void zero_offsets_kernel(int32_t* offsets, int n) {
 }  // namespace
 
 int64_t segments_workspace(int64_t n, int64_t G) {
-  const int64_t unit = unit_length(n);
-  return (n + unit - 1) / unit * (G + 1);
+  if (n <= kManyRun) return 0;
+  const int64_t run = run_length(n);
+  return (n + run - 1) / run * (G + 1);
 }
 
 hipError_t launch_segments(const SegmentArgs& a, hipStream_t s) {
@@ -122,14 +193,24 @@ hipError_t launch_segments(const SegmentArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(zero_offsets_kernel, dim3(1), dim3(64), 0, s, a.offsets, a.G + 1);
     return hipGetLastError();
   }
-  const int64_t unit = unit_length(a.n), units = (a.n + unit - 1) / unit;
   int bits = 0;
   while (a.G >> bits) ++bits;
-  const dim3 grid(static_cast<unsigned>((units + kUnitWaves - 1) / kUnitWaves)), block(kUnitWaves * 64);
-  hipLaunchKernelGGL(count_kernel, grid, block, 0, s, a, unit, bits);
+  if (a.n <= kFewRun) {
+    hipLaunchKernelGGL((place_kernel<kFewWaves, kFewRounds, true>), dim3(1), dim3(kFewWaves * 64), 0, s, a, kFewRun,
+                       bits);
+    return hipGetLastError();
+  }
+  if (a.n <= kManyRun) {
+    hipLaunchKernelGGL((place_kernel<kManyWaves, kManyRounds, true>), dim3(1), dim3(kManyWaves * 64), 0, s, a, kManyRun,
+                       bits);
+    return hipGetLastError();
+  }
+  const int64_t run = run_length(a.n);
+  const dim3 grid(static_cast<unsigned>((a.n + run - 1) / run)), block(kFewWaves * 64);
+  hipLaunchKernelGGL(count_kernel, grid, block, 0, s, a, run, bits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(place_kernel, grid, block, 0, s, a, unit, bits);
+  hipLaunchKernelGGL((place_kernel<kFewWaves, kFewRounds, false>), grid, block, 0, s, a, run, bits);
   return hipGetLastError();
 }
 

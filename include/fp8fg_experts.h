@@ -40,8 +40,8 @@ enum { FP8FG_SCORE_SOFTMAX = 0, FP8FG_SCORE_SIGMOID = 1 };
  * than k experts are left, the remaining places hold expert -1 with weight 0.  A logit
  * of -infinity has score 0; if all of a token's are, so are all its scores.  A c (without a
  * bias, a logit) that is not a number ranks below all numbers; scores that are not numbers
- * (of a NaN logit, and under softmax of its whole token, as of a logit of +infinity) show in
- * the weights.  Renormalised weights are shares of the scores as real numbers, also where
+ * (of a NaN logit, and under softmax all of its token's but those that are 0, as of a logit of
+ * +infinity) show in the weights.  Renormalised weights are shares of the scores as real numbers, also where
  * every chosen score is too small for fp32.
  *
  * logits       [T, E] of `dtype`, row pitch ld >= E elements.
