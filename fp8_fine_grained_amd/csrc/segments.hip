@@ -16,7 +16,7 @@
 namespace fp8fg {
 namespace {
 
-constexpr int kFewWaves = 4, kFewRounds = 4;      // 1024 entries: the workgroups of many, or a single small one
+constexpr int kFewWaves = 8, kFewRounds = 2;      // 1024 entries: the workgroups of many, or a single small one
 constexpr int kManyWaves = 16, kManyRounds = 8;   // 8192 entries: the most of a single workgroup
 constexpr int64_t kFewRun = kFewWaves * kFewRounds * 64, kManyRun = kManyWaves * kManyRounds * 64;
 constexpr int64_t kMostGroups = 1024;             // (longer inputs: longer runs)
@@ -57,13 +57,18 @@ __device__ __forceinline__ int rank_in(uint64_t m) {
 }
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
+// The lanes with the same bin, for every round that holds entries.
+template <int R>
+__device__ __forceinline__ void match(const int (&bin)[R], int64_t begin, int64_t end, int bits, uint64_t (&m)[R]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) m[r] = begin + 64 * r < end ? same_bin(bin[r], bits) : 0;
+}
 // Adds a wavefront's entries to its counts.
 template <int R>
-__device__ __forceinline__ void count(const int (&bin)[R], int bits, int32_t* c) {
+__device__ __forceinline__ void count(const int (&bin)[R], const uint64_t (&m)[R], int32_t* c) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const uint64_t m = same_bin(bin[r], bits);
-    if (m != 0 && rank_in(m) == 0) c[bin[r]] += __popcll(m);
+    if (m[r] != 0 && rank_in(m[r]) == 0) c[bin[r]] += __popcll(m[r]);
     wave_fence();
   }
 }
@@ -78,8 +83,10 @@ __global__ void __launch_bounds__(kFewWaves * 64) count_kernel(SegmentArgs a, in
   wave_fence();
   for (int64_t i = begin; i < end; i += kFewRounds * 64) {
     int bin[kFewRounds];
+    uint64_t m[kFewRounds];
     load_bins(a, i, end, bin);
-    count(bin, bits, c[wave]);
+    match(bin, i, end, bits, m);
+    count(bin, m, c[wave]);
   }
   __syncthreads();
   for (int g = threadIdx.x; g <= a.G; g += kFewWaves * 64) {
@@ -102,10 +109,17 @@ __global__ void __launch_bounds__(WAVES * 64) place_kernel(SegmentArgs a, int64_
   const int64_t begin = blockIdx.x * run + wave * part, end = begin + part < a.n ? begin + part : a.n;
   for (int g = lane; g < bins; g += 64) at[wave][g] = 0;
   wave_fence();
-  for (int64_t i = begin; i < end; i += R * 64) {
-    int bin[R];
-    load_bins(a, i, end, bin);
-    count(bin, bits, at[wave]);
+  int bin[R];           // of the first R * 64 entries, all of them but for very long inputs
+  uint64_t same[R];
+  if (begin < end) load_bins(a, begin, end, bin);
+  match(bin, begin, end, bits, same);
+  count(bin, same, at[wave]);
+  for (int64_t i = begin + R * 64; i < end; i += R * 64) {
+    int more[R];
+    uint64_t m[R];
+    load_bins(a, i, end, more);
+    match(more, i, end, bits, m);
+    count(more, m, at[wave]);
   }
   __syncthreads();
   for (int g = threadIdx.x; g < bins; g += WAVES * 64) {
@@ -157,11 +171,14 @@ __global__ void __launch_bounds__(WAVES * 64) place_kernel(SegmentArgs a, int64_
   }
   __syncthreads();
   for (int64_t i = begin; i < end; i += R * 64) {
-    int bin[R];
-    load_bins(a, i, end, bin);
+    if (i > begin) {
+      load_bins(a, i, end, bin);
+      match(bin, i, end, bits, same);
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint64_t m = same_bin(bin[r], bits);
+      if (i + 64 * r >= end) break;
+      const uint64_t m = same[r];
       const int rank = rank_in(m);
       const int64_t k = i + 64 * r + lane;
       if (m != 0) {
