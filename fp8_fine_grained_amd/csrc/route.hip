@@ -65,6 +65,31 @@ __device__ __forceinline__ void scores(bool sigmoidal, const float (&z)[STEPS], 
   }
 }
 
+// The sigmoid of a logit: 0 for -infinity, and what is not a number stays so.
+__device__ __forceinline__ float score(float z) {
+  const float v = z == z ? sigmoid(z) : z;
+  return z == -__builtin_inff() ? 0.0f : v;
+}
+
+// Reductions over aligned groups of L = 16 or 64 lanes.
+template <int L>
+__device__ __forceinline__ float max_of(float v) {
+  v = max16(v);
+  if constexpr (L == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float sum_of(float v) {
+  if constexpr (L == 64) return sum64(v);
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  return v + dpp<0x140>(v);
+}
+
 // A chosen expert's score times a factor that is the same for all of its token's (m: the
 // largest chosen logit), for their shares: fp32 holds it however small the scores are.
 __device__ __forceinline__ float share(bool sigmoidal, float z, float m) {
@@ -75,8 +100,8 @@ __device__ __forceinline__ float share(bool sigmoidal, float z, float m) {
 // Lane j < k: the share of the j-th chosen expert's logit among them; the other lanes (and
 // places without an expert) hold -infinity.
 __device__ __forceinline__ float shares(bool sigmoidal, float z) {
-  const float f = share(sigmoidal, z, wave_max(z));
-  const float sum = wave_sum(f);
+  const float f = share(sigmoidal, z, max_of<64>(z));
+  const float sum = sum64(f);
   return f == 0.0f ? 0.0f : f / sum;
 }
 
@@ -196,25 +221,6 @@ __global__ void __launch_bounds__(kWaves * 64) route_wide_kernel(RouteArgs a) {
 }
 
 // ---------------------------------------------------------------- the fast kernel
-// Reductions over aligned groups of L = 16 or 64 lanes.
-template <int L>
-__device__ __forceinline__ float max_of(float v) {
-  v = max16(v);
-  if constexpr (L == 64) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    v = fmaxf(v, __shfl_xor(v, 32));
-  }
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float sum_of(float v) {
-  if constexpr (L == 64) return sum64(v);
-  v += dpp<0xB1>(v);
-  v += dpp<0x4E>(v);
-  v += dpp<0x141>(v);
-  return v + dpp<0x140>(v);
-}
-
 // Signed integers in the order of finite floats (without -0), and back: the same exchange.
 __device__ __forceinline__ int ordered(int b) { return b ^ ((b >> 31) & 0x7FFFFFFF); }
 __device__ __forceinline__ int dpp_max(int v, int o) { return o > v ? o : v; }
@@ -334,8 +340,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float v = z[i] == z[i] ? sigmoid(z[i]) : z[i];
-          s[i] = z[i] == -kInf ? 0.0f : v;
+          s[i] = score(z[i]);
         }
       } else {
         top = -kInf;
@@ -372,7 +377,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
     if (grouped) {
       // the two largest choices of every group
       auto choice = [&](int i) { return BIAS || !sums || key[i] == -kInf ? key[i] : s[i]; };
-      float* score = group_score[wave][slot];
+      float* of_group = group_score[wave][slot];
       if (whole) {
         float first = -kInf, second = -kInf;
 #pragma unroll
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
         if (lanes >= 8) merge_two(first, second, dpp<0x141>(first), dpp<0x141>(second));
         if (lanes >= 16) merge_two(first, second, dpp<0x140>(first), dpp<0x140>(second));
         if ((l & (lanes - 1)) == 0 && e0 < a.E)
-          score[e0 / size] = !sums ? first : second == -kInf ? -kInf : first + second;
+          of_group[e0 / size] = !sums ? first : second == -kInf ? -kInf : first + second;
       } else {
         float* c = narrow[wave][slot];
 #pragma unroll
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
             merge_one(first, second, c[g * size + at]);
             at = at + 1 == size ? 0 : at + 1;
           }
-          score[g] = !sums ? first : second == -kInf ? -kInf : first + second;
+          of_group[g] = !sums ? first : second == -kInf ? -kInf : first + second;
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -405,9 +410,9 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       float low = kInf, high = -kInf;
       for (int g0 = 0; g0 < a.groups; g0 += L) {
         const int g = g0 + l;
-        const float mine = g < a.groups ? score[g] : -kInf;
+        const float mine = g < a.groups ? of_group[g] : -kInf;
         int before = 0;
-        for (int o = 0; o < a.groups; ++o) before += score[o] > mine ? 1 : 0;
+        for (int o = 0; o < a.groups; ++o) before += of_group[o] > mine ? 1 : 0;
         const bool keep = mine > -kInf && before < a.kept;
         stay |= of_token(__ballot(keep)) << g0;
         if (keep)
@@ -517,65 +522,73 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
 }
 
 // ---------------------------------------------------------------- gradient
-// One wavefront per token; lane j holds the j-th chosen expert's t.
-template <bool BF16>
+// One wavefront per token, STEPS experts per lane; lane j holds the j-th chosen expert's t, and hands it to the lane of
+// the expert (one scalar comparison per step, no search).  Bound by HBM at large T: the logits in, their gradient out.
+template <bool BF16, int STEPS>
 __global__ void __launch_bounds__(kWaves * 64) route_backward_kernel(RouteGradArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float out = -__builtin_inff();
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + wave; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * kWaves) {
-    float z[kSteps], s[kSteps], d[kSteps];
+    int mine = lane < a.k ? a.experts[t * a.k + lane] : -1;
+    float dw = lane < a.k ? a.dw[t * a.k + lane] : 0.0f;
+    float z[STEPS], s[STEPS], d[STEPS];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
       const int e = lane + 64 * i;
       z[i] = e < a.E ? element<BF16>(a.z, t * a.ld + e) : out;
+      d[i] = a.ds && e < a.E ? a.ds[t * a.E + e] : 0.0f;
     }
-    scores<float, kSteps>(a.sigmoid, z, s);
-    int mine = lane < a.k ? a.experts[t * a.k + lane] : -1;
     if (mine >= a.E) mine = -1;
-    const float dw = mine >= 0 ? a.scale * a.dw[t * a.k + lane] : 0.0f;
+    dw = mine >= 0 ? a.scale * dw : 0.0f;
+    const float zc = mine >= 0 ? element<BF16>(a.z, t * a.ld + mine) : out;  // (on its way before the scores)
+    float top = out, total = 1.0f;
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) s[i] = score(z[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) top = fmaxf(top, z[i]);
+      top = max_of<64>(top);
+      total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        s[i] = z[i] == out ? 0.0f : expf(z[i] - top);
+        total += s[i];
+      }
+      total = sum64(total);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) s[i] = s[i] == 0.0f ? 0.0f : s[i] / total;
+    }
     float tj;
     if (a.renormalise) {
-      const float p = shares(a.sigmoid, mine >= 0 ? element<BF16>(a.z, t * a.ld + mine) : out);
-      tj = p * (dw - wave_sum(dw * p));
+      const float p = shares(a.sigmoid, zc);
+      tj = p * (dw - sum64(dw * p));
     } else {
-      float chosen = 0.0f;
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __builtin_amdgcn_readfirstlane(__shfl(mine, j));
-        if (e < 0) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-          if (i == (e >> 6)) v = s[i];
-        v = __shfl(v, e & 63);
-        if (lane == j) chosen = v;
-      }
-      tj = chosen * dw;
+      const float f = a.sigmoid ? score(zc) : zc == out ? 0.0f : expf(zc - top) / total;
+      tj = f * dw;
     }
-    float total = 0.0f;
+    float u = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int e = lane + 64 * i;
-      d[i] = a.ds && e < a.E ? a.ds[t * a.E + e] * s[i] : 0.0f;
-      total += d[i];
+    for (int i = 0; i < STEPS; ++i) {
+      d[i] = a.ds ? d[i] * s[i] : 0.0f;
+      u += d[i];
     }
     for (int j = 0; j < a.k; ++j) {
-      const int e = __builtin_amdgcn_readfirstlane(__shfl(mine, j));
-      const float v = __shfl(tj, j);
+      const int e = __builtin_amdgcn_readlane(mine, j);
+      const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(tj), j));
       if (e < 0) continue;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        if (i == (e >> 6) && lane == (e & 63)) d[i] += v;
+      for (int i = 0; i < STEPS; ++i)
+        if (i == (e >> 6)) d[i] += lane == (e & 63) ? v : 0.0f;
     }
-    if (!a.sigmoid) {
-      // (renormalised weights do not change with a common factor: their t sum to zero)
-      total = wave_sum(a.renormalise ? total : total + tj);
-    }
+    // (renormalised weights do not change with a common factor: their t sum to zero)
+    if (!a.sigmoid) u = sum64(a.renormalise ? u : u + tj);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
       const int e = lane + 64 * i;
       if (e >= a.E) continue;
-      float v = a.sigmoid ? d[i] * (1.0f - s[i]) : d[i] - s[i] * total;
+      float v = a.sigmoid ? d[i] * (1.0f - s[i]) : d[i] - s[i] * u;
       if (z[i] == out) v = 0.0f;
       if constexpr (BF16)
         static_cast<uint16_t*>(a.dz)[t * a.E + e] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
@@ -620,11 +633,20 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t s) {
-  if (a.bf16)
-    hipLaunchKernelGGL(route_backward_kernel<true>, token_blocks(a.T), dim3(kWaves * 64), 0, s, a);
-  else
-    hipLaunchKernelGGL(route_backward_kernel<false>, token_blocks(a.T), dim3(kWaves * 64), 0, s, a);
-  return hipGetLastError();
+  auto form = [&](auto bf16) {
+    constexpr bool BF16 = decltype(bf16)::value;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, token_blocks(a.T), dim3(kWaves * 64), 0, s, a); };
+    if (a.E <= 64)
+      go(route_backward_kernel<BF16, 1>);
+    else if (a.E <= 128)
+      go(route_backward_kernel<BF16, 2>);
+    else if (a.E <= 256)
+      go(route_backward_kernel<BF16, 4>);
+    else
+      go(route_backward_kernel<BF16, 16>);
+    return hipGetLastError();
+  };
+  return a.bf16 ? form(std::true_type{}) : form(std::false_type{});
 }
 
 }  // namespace fp8fg
