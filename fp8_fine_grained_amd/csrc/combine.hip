@@ -117,15 +117,18 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a, int64_
   }
 }
 
-// A workgroup per token: its wavefronts take the pieces in turn, J places at a time, so that dy is read once for all of
-// them and J rows' loads are in flight; the dot products' parts meet in LDS, in the order of the wavefronts.
+// W wavefronts per token take the pieces in turn, J places at a time, so that dy is read once for all of them and J
+// rows' loads are in flight; the dot products' parts meet in LDS, in the order of the wavefronts.  One wavefront does
+// for short rows (100000 tokens of 2 x 256: 311 -> xx us), sixteen share few tokens (one of 8 x 7168: 8.5 -> x us).
 // DW: dweights are asked for (the rows are read).
-template <bool BF16, bool QUANT, bool DW, int J>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(CombineGradArgs a) {
+template <bool BF16, bool QUANT, bool DW, int J, int W>
+__global__ void __launch_bounds__(W == 1 ? kThreads : W * 64) combine_backward_kernel(CombineGradArgs a) {
+  constexpr int TOKENS = W == 1 ? kPerGroup : 1;  // of a workgroup
   using P = Piece<BF16>;
   using O = Octet<BF16>;
-  __shared__ float part[kPerGroup][J];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ float part[W][J];
+  const int lane = threadIdx.x & 63, id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = W == 1 ? 0 : id;
   const int64_t pieces = (a.H + 511) / 512, G = a.H / 128;
   // QUANT: a lane's octet of the group g = base / 128 + lane / 16; groups past the row's end read the first
   auto load = [&](auto nt, const void* row, int64_t base) {
@@ -148,7 +151,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(CombineGradA
       P::cut(f, base, lane, a.H);
     }
   };
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * TOKENS + (W == 1 ? id : 0); t < a.T;
+       t += static_cast<int64_t>(gridDim.x) * TOKENS) {
     const char* dy = static_cast<const char*>(a.dy) + t * a.ld_dy * P::ES;
     int p = lane < a.k ? a.positions[t * a.k + lane] : -1;
     const float w = lane < a.k ? (a.weights ? a.weights[t * a.k + lane] : 1.0f) : 0.0f;
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(CombineGradA
       float dot[J];
 #pragma unroll
       for (int j = 0; j < J; ++j) dot[j] = 0.0f;
-      for (int64_t piece = wave; piece < pieces; piece += kPerGroup) {
+      for (int64_t piece = wave; piece < pieces; piece += W) {
         const int64_t base = piece * 512;
         decltype(load(std::true_type{}, dy, base)) r[DW ? J : 1];
         const auto rd = load(std::false_type{}, dy, base);
@@ -206,15 +210,17 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(CombineGradA
           const float v = sum64(dot[j]);
           if (lane == j) mine = v;
         }
-        if (lane < J) part[wave][lane] = mine;
-        __syncthreads();
-        if (wave == 0 && lane < J && j0 + lane < a.k) {
-          float v = part[0][lane];
+        if constexpr (W > 1) {
+          if (lane < J) part[wave][lane] = mine;
+          __syncthreads();
+          if (wave == 0 && lane < J) {
+            mine = part[0][lane];
 #pragma unroll
-          for (int q = 1; q < kPerGroup; ++q) v += part[q][lane];
-          a.dw[t * a.k + j0 + lane] = v;
+            for (int q = 1; q < W; ++q) mine += part[q][lane];
+          }
+          __syncthreads();
         }
-        __syncthreads();
+        if (wave == 0 && lane < J && j0 + lane < a.k) a.dw[t * a.k + j0 + lane] = mine;
       }
     }
   }
@@ -229,11 +235,12 @@ hipError_t launch_combine(const CombineArgs& args, hipStream_t s) {
   if (a.R == 0) a.k = 0;  // (no row to read in a place's stead)
   const int64_t pieces = (a.H + 511) / 512;
   const dim3 grid(blocks((a.T * pieces + kPerGroup - 1) / kPerGroup));
-  if (a.bf16)
-    hipLaunchKernelGGL((combine_kernel<true, 8>), grid, dim3(kThreads), 0, s, a, pieces);
-  else
-    hipLaunchKernelGGL((combine_kernel<false, 4>), grid, dim3(kThreads), 0, s, a, pieces);
-  return hipGetLastError();
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, a, pieces);
+    return hipGetLastError();
+  };
+  if (a.bf16) return a.k <= 2 ? go(combine_kernel<true, 2>) : a.k <= 4 ? go(combine_kernel<true, 4>) : go(combine_kernel<true, 8>);
+  return a.k <= 2 ? go(combine_kernel<false, 2>) : go(combine_kernel<false, 4>);
 }
 
 hipError_t launch_combine_backward(const CombineGradArgs& args, hipStream_t s) {
@@ -244,16 +251,34 @@ hipError_t launch_combine_backward(const CombineGradArgs& args, hipStream_t s) {
     a.ld_rows = 0;
     a.drows = nullptr;
   }
-  const dim3 grid(blocks(a.T));
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, a); };
-  auto form = [&](auto bf16, auto quant) {
-    constexpr bool BF16 = decltype(bf16)::value, QUANT = decltype(quant)::value;
-    a.dw ? go(combine_backward_kernel<BF16, QUANT, true, BF16 ? 8 : 4>)
-         : go(combine_backward_kernel<BF16, QUANT, false, BF16 ? 8 : 4>);
+  const int64_t pieces = (a.H + 511) / 512;
+  // Wavefronts per token: one for rows of one piece, sixteen where the tokens are fewer than the compute units.
+  const int w = pieces <= 1 ? 1 : a.T <= 128 ? 16 : 4;
+  auto form = [&](auto bf16, auto quant, auto dw) {
+    constexpr bool BF16 = decltype(bf16)::value, QUANT = decltype(quant)::value, DW = decltype(dw)::value;
+    auto go = [&](auto j) {
+      constexpr int J = decltype(j)::value;
+      const dim3 grid(blocks(w == 1 ? (a.T + kPerGroup - 1) / kPerGroup : a.T));
+      if (w == 1)
+        hipLaunchKernelGGL((combine_backward_kernel<BF16, QUANT, DW, J, 1>), grid, dim3(kThreads), 0, s, a);
+      else if (w == 4)
+        hipLaunchKernelGGL((combine_backward_kernel<BF16, QUANT, DW, J, 4>), grid, dim3(256), 0, s, a);
+      else
+        hipLaunchKernelGGL((combine_backward_kernel<BF16, QUANT, DW, J, 16>), grid, dim3(1024), 0, s, a);
+    };
+    if (a.k <= 2)
+      go(std::integral_constant<int, 2>{});
+    else if (a.k <= 4 || !BF16)  // (an fp32 piece takes twice the registers)
+      go(std::integral_constant<int, 4>{});
+    else
+      go(std::integral_constant<int, 8>{});
     return hipGetLastError();
   };
-  if (a.scales) return a.bf16 ? form(std::true_type{}, std::true_type{}) : form(std::false_type{}, std::true_type{});
-  return a.bf16 ? form(std::true_type{}, std::false_type{}) : form(std::false_type{}, std::false_type{});
+  auto outputs = [&](auto bf16, auto quant) {
+    return a.dw ? form(bf16, quant, std::true_type{}) : form(bf16, quant, std::false_type{});
+  };
+  if (a.scales) return a.bf16 ? outputs(std::true_type{}, std::true_type{}) : outputs(std::false_type{}, std::true_type{});
+  return a.bf16 ? outputs(std::true_type{}, std::false_type{}) : outputs(std::false_type{}, std::false_type{});
 }
 
 }  // namespace fp8fg

@@ -71,23 +71,23 @@ __device__ __forceinline__ float score(float z) {
   return z == -__builtin_inff() ? 0.0f : v;
 }
 
-// Reductions over aligned groups of L = 16 or 64 lanes.
+// Reductions over aligned groups of L = 16, 32 or 64 lanes.
 template <int L>
 __device__ __forceinline__ float max_of(float v) {
   v = max16(v);
-  if constexpr (L == 64) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    v = fmaxf(v, __shfl_xor(v, 32));
-  }
+  if constexpr (L >= 32) v = fmaxf(v, __shfl_xor(v, 16));
+  if constexpr (L == 64) v = fmaxf(v, __shfl_xor(v, 32));
   return v;
 }
 template <int L>
 __device__ __forceinline__ float sum_of(float v) {
-  if constexpr (L == 64) return sum64(v);
   v += dpp<0xB1>(v);
   v += dpp<0x4E>(v);
   v += dpp<0x141>(v);
-  return v + dpp<0x140>(v);
+  v += dpp<0x140>(v);
+  if constexpr (L >= 32) v += __shfl_xor(v, 16);
+  if constexpr (L == 64) v += __shfl_xor(v, 32);
+  return v;
 }
 
 // A chosen expert's score times a factor that is the same for all of its token's (m: the
@@ -230,10 +230,8 @@ __device__ __forceinline__ int max_of(int v) {
   v = dpp_max(v, __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, false));
   v = dpp_max(v, __builtin_amdgcn_update_dpp(v, v, 0x141, 0xF, 0xF, false));
   v = dpp_max(v, __builtin_amdgcn_update_dpp(v, v, 0x140, 0xF, 0xF, false));
-  if constexpr (L == 64) {
-    v = dpp_max(v, __shfl_xor(v, 16));
-    v = dpp_max(v, __shfl_xor(v, 32));
-  }
+  if constexpr (L >= 32) v = dpp_max(v, __shfl_xor(v, 16));
+  if constexpr (L == 64) v = dpp_max(v, __shfl_xor(v, 32));
   return v;
 }
 // Descending order of a lane's keys: odd-even merging (63 exchanges of a maximum and a minimum for 16 keys).
@@ -275,8 +273,8 @@ __device__ __forceinline__ void merge_two(float& first, float& second, float f, 
 //  * bf16 logits without a bias leave room for the whole index: the keys are exact, ties and all;
 //  * other keys give up four bits for the place in the lane.  Neighbours that lie closer than those bits and the
 //    rounding of a score are put in order by their 64-bit values.  Where that does not do (three in one place at the
-//    border, groups that lie close, softmax with a bias) the token is done again in 64 bits, and so is one with a
-//    value that is not a number or +infinity.
+//    border, sums of groups that lie close) the token is done again in 64 bits, and so is one with a value that is not
+//    a number or +infinity.
 // Bound by the instructions of the k rounds, not by the logits' bytes; four tokens share a wavefront because a round
 // costs the same for one (8192 x 256 in 8 groups: a wavefront per token, all in 64 bits, took 130 us).
 template <bool BF16, bool BIAS, int L, int V>
@@ -290,7 +288,8 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (L - 1), slot = lane / L;
   const int e0 = l * V;
-  auto of_token = [&](uint64_t ballot) -> uint64_t { return L == 64 ? ballot : (ballot >> (slot * L)) & 0xFFFF; };
+  constexpr uint64_t kToken = L == 64 ? ~uint64_t(0) : (uint64_t(1) << (L & 63)) - 1;  // lanes of the first token
+  auto of_token = [&](uint64_t ballot) -> uint64_t { return L == 64 ? ballot : (ballot >> (slot * L)) & kToken; };
   float bias[BIAS ? V : 1];
   if constexpr (BIAS) {
 #pragma unroll
@@ -404,15 +403,20 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      // groups with fewer than `kept` larger ones stay; the smallest that stays and the largest that does not have to
-      // be told apart (equal ones are left to the 64-bit form)
+      // Groups with fewer than `kept` before them stay.  Maxima of logits compare exactly; of scores and sums the
+      // smallest that stays and the largest that does not have to be told apart (equal ones are left to the 64-bit
+      // form).
+      const bool exact = !BIAS && !sums;
       uint64_t stay = 0;
       float low = kInf, high = -kInf;
       for (int g0 = 0; g0 < a.groups; g0 += L) {
         const int g = g0 + l;
         const float mine = g < a.groups ? of_group[g] : -kInf;
         int before = 0;
-        for (int o = 0; o < a.groups; ++o) before += of_group[o] > mine ? 1 : 0;
+        for (int o = 0; o < a.groups; ++o) {
+          const float other = of_group[o];
+          before += other > mine || (exact && other == mine && o < g) ? 1 : 0;
+        }
         const bool keep = mine > -kInf && before < a.kept;
         stay |= of_token(__ballot(keep)) << g0;
         if (keep)
@@ -422,8 +426,8 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       }
       low = -max_of<L>(-low);
       high = max_of<L>(high);
-      const float apart = BIAS || sums ? 4.0f * off + 0x1p-22f * fmaxf(fabsf(low), fabsf(high)) : 0.0f;
-      again |= (high > -kInf && !(low - high > apart)) || __popcll(stay) > a.kept;
+      const float apart = 4.0f * off + 0x1p-22f * fmaxf(fabsf(low), fabsf(high));
+      again |= !exact && ((high > -kInf && !(low - high > apart)) || __popcll(stay) > a.kept);
       int g = e0 / size, next = (g + 1) * size;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -470,16 +474,23 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
     }
     if constexpr (!EXACT) {
       // Neighbours that the keys cannot tell apart, found in any order: in the order of the logits themselves, or of
-      // 64-bit sums (of softmax scores the whole token's: done again).
-      if (BIAS && !a.sigmoid) {
-        again |= close;
-        close = false;
-      }
+      // 64-bit sums.
       if (__ballot(close)) {
+        double all = 1.0;
+        if (BIAS && !a.sigmoid) {
+          all = 0.0;
+#pragma unroll 1
+          for (int e = e0; e < e0 + V && e < a.E; ++e)
+            all += exp(static_cast<double>(element<BF16>(a.z, t * a.ld + e)) - static_cast<double>(top));
+#pragma unroll
+          for (int d = 1; d < L; d <<= 1) all += __shfl_xor(all, d);
+        }
         double c = -__builtin_inf();
         if (mine >= 0) {
           c = static_cast<double>(element<BF16>(a.z, t * a.ld + mine));
-          if constexpr (BIAS) c = 1.0 / (1.0 + exp(-c)) + static_cast<double>(a.bias[mine]);
+          if constexpr (BIAS)
+            c = (a.sigmoid ? 1.0 / (1.0 + exp(-c)) : exp(c - static_cast<double>(top)) / all) +
+                static_cast<double>(a.bias[mine]);
         }
         int place = 0;
         for (int o = 0; o < found; ++o) {
@@ -516,7 +527,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
     if (redo) {
 #pragma unroll 1
       for (int q = 0; q < TOKENS; ++q)
-        if (L == 64 || ((redo >> (q * L)) & 0xFFFF)) route_token<BF16>(a, t0 + q, wide[wave]);
+        if ((redo >> (q * L)) & kToken) route_token<BF16>(a, t0 + q, wide[wave]);
     }
   }
 }
@@ -615,7 +626,8 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   }
   auto shape = [&](auto bf16, auto bias) {
     constexpr bool BF16 = decltype(bf16)::value, BIAS = decltype(bias)::value;
-    const dim3 narrow = token_blocks((a.T + 3) / 4), full = token_blocks(a.T), block(kWaves * 64);
+    const dim3 narrow = token_blocks((a.T + 3) / 4), half = token_blocks((a.T + 1) / 2), full = token_blocks(a.T),
+               block(kWaves * 64);
     if (a.E <= 64)
       hipLaunchKernelGGL((route_kernel<BF16, BIAS, 16, 4>), narrow, block, 0, s, a);
     else if (a.E <= 128)
@@ -623,7 +635,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
     else if (a.E <= 256)
       hipLaunchKernelGGL((route_kernel<BF16, BIAS, 16, 16>), narrow, block, 0, s, a);
     else if (a.E <= 512)
-      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 64, 8>), full, block, 0, s, a);
+      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 32, 16>), half, block, 0, s, a);
     else
       hipLaunchKernelGGL((route_kernel<BF16, BIAS, 64, 16>), full, block, 0, s, a);
     return hipGetLastError();
@@ -642,6 +654,8 @@ hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t s) {
       go(route_backward_kernel<BF16, 2>);
     else if (a.E <= 256)
       go(route_backward_kernel<BF16, 4>);
+    else if (a.E <= 512)
+      go(route_backward_kernel<BF16, 8>);
     else
       go(route_backward_kernel<BF16, 16>);
     return hipGetLastError();

@@ -102,16 +102,38 @@ template <int WAVES, int R, bool ONE>
 __global__ void __launch_bounds__(WAVES * 64) place_kernel(SegmentArgs a, int64_t run, int bits) {
   __shared__ int32_t at[WAVES][kSegmentMaxG + 1];  // counts, then where the wavefront's next entry of a bin goes
   __shared__ int32_t start[kSegmentMaxG + 1];
+  __shared__ int32_t base[ONE ? 1 : kSegmentMaxG + 1];
   __shared__ int32_t chunk[(kSegmentMaxG + 64) / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int bins = a.G + 1;
   const int64_t part = run / WAVES;
   const int64_t begin = blockIdx.x * run + wave * part, end = begin + part < a.n ? begin + part : a.n;
   for (int g = lane; g < bins; g += 64) at[wave][g] = 0;
-  wave_fence();
   int bin[R];           // of the first R * 64 entries, all of them but for very long inputs
   uint64_t same[R];
   if (begin < end) load_bins(a, begin, end, bin);
+  // The table's sums: entries of all workgroups, and of those before this one.  (Their loads go out with the entries'
+  // own: one latency instead of two.)
+  if constexpr (!ONE) {
+    const int groups = gridDim.x, mine = blockIdx.x;
+    for (int g = threadIdx.x; g < bins; g += WAVES * 64) {
+      int32_t before = 0, total = 0;
+      for (int b0 = 0; b0 < groups; b0 += 16) {
+        int32_t v[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = a.counts[static_cast<int64_t>(b0 + q < groups ? b0 + q : 0) * bins + g];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int32_t c = b0 + q < groups ? v[q] : 0;
+          total += c;
+          before += b0 + q < mine ? c : 0;
+        }
+      }
+      start[g] = total;
+      base[g] = before;
+    }
+  }
+  wave_fence();
   match(bin, begin, end, bits, same);
   count(bin, same, at[wave]);
   for (int64_t i = begin + R * 64; i < end; i += R * 64) {
@@ -123,29 +145,15 @@ __global__ void __launch_bounds__(WAVES * 64) place_kernel(SegmentArgs a, int64_
   }
   __syncthreads();
   for (int g = threadIdx.x; g < bins; g += WAVES * 64) {
-    int32_t before = 0, total = 0;
-    if constexpr (!ONE) {
-      const int groups = gridDim.x, mine = blockIdx.x;
-      for (int b0 = 0; b0 < groups; b0 += 32) {  // 32 loads in flight
-        int32_t v[32];
-#pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] = a.counts[static_cast<int64_t>(b0 + q < groups ? b0 + q : 0) * bins + g];
-#pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const int32_t c = b0 + q < groups ? v[q] : 0;
-          total += c;
-          before += b0 + q < mine ? c : 0;
-        }
-      }
-    }
     // the wavefronts' counts become the counts before them
+    int32_t before = ONE ? 0 : base[g];
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
       const int32_t c = at[w][g];
       at[w][g] = before;
       before += c;
     }
-    start[g] = ONE ? before : total;
+    if constexpr (ONE) start[g] = before;
   }
   __syncthreads();
   // exclusive sums of the bins' totals, a chunk of 64 per wavefront, then over the chunks

@@ -61,8 +61,7 @@ def lib():
     return _lib
 
 
-def _score_code(score):
-    return {"softmax": SOFTMAX, "sigmoid": SIGMOID, SOFTMAX: SOFTMAX, SIGMOID: SIGMOID}[score]
+_SCORES = {"softmax": SOFTMAX, "sigmoid": SIGMOID, SOFTMAX: SOFTMAX, SIGMOID: SIGMOID}
 
 
 # ------------------------------------------------------------------ routing
@@ -100,7 +99,7 @@ def route_experts(logits, k, bias=None, mask=None, score="sigmoid", groups=1, gr
     elif need_scores:
         scores = logits.new_empty((T, E), dtype=torch.float32)
     st = (_lib or lib()).fp8fg_route_experts(
-        logits.data_ptr(), _dtype_code(logits.dtype), T, E, _ld(logits), _ptr(bias), _ptr(mask), _score_code(score),
+        logits.data_ptr(), _dtype_code(logits.dtype), T, E, _ld(logits), _ptr(bias), _ptr(mask), _SCORES[score],
         groups, groups_kept, group_terms, k, 1 if renormalise else 0, scale, experts.data_ptr(), weights.data_ptr(),
         _ptr(scores), _stream(logits))
     _check("fp8fg_route_experts", st)
@@ -130,7 +129,7 @@ def route_experts_backward(dweights, experts, logits, score="sigmoid", renormali
         _given("dlogits", logits.dtype, (T, E), dlogits)
     st = (_lib or lib()).fp8fg_route_experts_backward(
         dweights.data_ptr(), experts.data_ptr(), logits.data_ptr(), _dtype_code(logits.dtype), T, E, _ld(logits),
-        _score_code(score), k, 1 if renormalise else 0, scale, _ptr(dscores), dlogits.data_ptr(), _stream(logits))
+        _SCORES[score], k, 1 if renormalise else 0, scale, _ptr(dscores), dlogits.data_ptr(), _stream(logits))
     _check("fp8fg_route_experts_backward", st)
     return dlogits
 
@@ -157,7 +156,7 @@ def expert_segments(experts, G, first=0, offsets=None, row_index=None, positions
     else:
         _given("row_index", torch.int32, (T * k,), row_index)
     if positions is None:
-        positions = experts.new_empty((T, k))
+        positions = torch.empty_like(experts)
     else:
         _given("positions", torch.int32, (T, k), positions)
     L = _lib or lib()
