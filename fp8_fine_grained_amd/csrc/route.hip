@@ -256,35 +256,42 @@ __device__ __forceinline__ void sort_keys(int (&k)[V]) {
   }
 }
 
-// The two largest of a set, of which v, or another part's two largest f and s, are met.
-__device__ __forceinline__ void merge_one(float& first, float& second, float v) {
-  second = fmaxf(second, fminf(first, v));
-  first = fmaxf(first, v);
+template <int CTRL>
+__device__ __forceinline__ int dpp_int(int v) {
+  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ void merge_two(float& first, float& second, float f, float s) {
-  second = fmaxf(fminf(first, f), fmaxf(second, s));
-  first = fmaxf(first, f);
+// The two largest of a set, of which v, or another part's two largest f and s, are met.
+__device__ __forceinline__ int larger(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ void merge_one(int& first, int& second, int v) {
+  second = larger(second, first < v ? first : v);
+  first = larger(first, v);
+}
+__device__ __forceinline__ void merge_two(int& first, int& second, int f, int s) {
+  second = larger(first < f ? first : f, larger(second, s));
+  first = larger(first, f);
 }
 
 // L lanes per token, V consecutive experts per lane (so that the lowest index is the first lane's first).  Choices go
 // through 32-bit keys, in the order of the fp32 values, whose low bits say where they come from.  A lane sorts its keys
-// once; then each round takes the largest of the lanes' first keys, and the lane it came from moves up by one.  (Unsorted
-// keys, searched and struck out in every round: 15.1 us instead of 1x at 8192 x 256.)
+// once; then each round takes the largest of the lanes' first keys, and the lane it came from moves up by one.
+// (Unsorted keys, searched and struck out in every round: 15.1 us instead of 12.2 at 8192 x 256.)
 //  * bf16 logits without a bias leave room for the whole index: the keys are exact, ties and all;
 //  * other keys give up four bits for the place in the lane.  Neighbours that lie closer than those bits and the
 //    rounding of a score are put in order by their 64-bit values.  Where that does not do (three in one place at the
 //    border, sums of groups that lie close) the token is done again in 64 bits, and so is one with a value that is not
 //    a number or +infinity.
-// Bound by the instructions of the k rounds, not by the logits' bytes; four tokens share a wavefront because a round
-// costs the same for one (8192 x 256 in 8 groups: a wavefront per token, all in 64 bits, took 130 us).
+// Bound by the instructions of its rounds and their fetch, not by the logits' bytes (8192 x 256 fp32 in 8 groups 12.2 us,
+// 1.7 for the bytes), so four tokens of up to 256 experts share a wavefront: a round costs the same for one.  (A
+// wavefront per token, all in 64 bits: 83 us.)
 template <bool BF16, bool BIAS, int L, int V>
 __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
   constexpr bool EXACT = BF16 && !BIAS;
   constexpr int TOKENS = 64 / L;
   constexpr float kInf = __builtin_inff();
+  constexpr int kOut = static_cast<int>(0x80000000), kLowest = static_cast<int>(0x80800000);  // (the largest negative)
   __shared__ double wide[kWaves][L * V];             // of tokens that are done again
-  __shared__ float narrow[kWaves][TOKENS][L * V];    // choices, where groups lie across lanes
-  __shared__ float group_score[kWaves][TOKENS][kRouteMaxGroups];
+  __shared__ int narrow[kWaves][TOKENS][L * V];    // choices, where groups lie across lanes
+  __shared__ __attribute__((aligned(16))) float group_score[kWaves][TOKENS][kRouteMaxGroups + 4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (L - 1), slot = lane / L;
   const int e0 = l * V;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       }
     }
   }
-  const int size = a.E / a.groups, lanes = size / V;
+  const int size = a.E / a.groups, lanes = size / V, shift = lanes > 0 ? __builtin_ctz(lanes) : 0;
   const bool grouped = a.kept < a.groups;
   const bool sums = grouped && a.terms == 2;  // sums of two scores are compared
   const bool whole = size % V == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 16;  // a group is 1, 2, 4, .. lanes
@@ -315,24 +322,26 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
   for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * TOKENS; t0 < a.T; t0 += stride) {
     const bool live = t0 + slot < a.T;
     const int64_t t = live ? t0 + slot : a.T - 1;  // past the end: the last token again, not stored
+    int E = a.E;
+    asm volatile("" : "+s"(E));  // (else its comparisons leave the loop, and fill and spill scalar registers)
     float z[V];
     if (vector) {
       if constexpr (V % VEC == 0) {
 #pragma unroll
         for (int q = 0; q < V / VEC; ++q) {
-          const int e = e0 + q * VEC < a.E ? e0 + q * VEC : 0;
+          const int e = e0 + q * VEC < E ? e0 + q * VEC : 0;
           const u32x4 u =
               *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.z) + (t * a.ld + e) * (BF16 ? 2 : 4));
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             uint32_t v = BF16 ? (i % 2 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16) : u[i % 4];
-            z[q * VEC + i] = e0 + q * VEC < a.E ? __uint_as_float(v) : -kInf;
+            z[q * VEC + i] = e0 + q * VEC < E ? __uint_as_float(v) : -kInf;
           }
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) z[i] = e0 + i < a.E ? element<BF16>(a.z, t * a.ld + e0 + i) : -kInf;
+      for (int i = 0; i < V; ++i) z[i] = e0 + i < E ? element<BF16>(a.z, t * a.ld + e0 + i) : -kInf;
     }
     float s[V], top = 0.0f, total = 1.0f, largest = 1.0f;
     if (scored) {
@@ -360,62 +369,71 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       if (a.scores && live) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (e0 + i < a.E) a.scores[t * a.E + e0 + i] = s[i];
+          if (e0 + i < E) a.scores[t * E + e0 + i] = s[i];
       }
     }
     // how far an fp32 score may be off: the sigmoid's roundings; or exponential, argument, sum and quotient
     const float off = a.sigmoid ? 0x1p-23f : 0x1p-18f * largest;
-    bool again = false;
-    float key[V];
+    // Choices as ordered integers; the tests of all of them at once: what is not a number lies beyond an infinity.
+    int ord[V], most = kLowest, least = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      key[i] = BIAS ? s[i] + bias[i] : z[i] + 0.0f;  // (no -0: it equals 0)
-      if (BIAS && z[i] == -kInf) key[i] = -kInf;
-      again |= !(key[i] < kInf);  // not a number, or +infinity
+      float c = BIAS ? s[i] + bias[i] : z[i] + 0.0f;  // (no -0: it equals 0)
+      if (BIAS && z[i] == -kInf) c = -kInf;
+      ord[i] = ordered(__float_as_int(c));
+      most = ord[i] > most ? ord[i] : most;
+      least = ord[i] < least ? ord[i] : least;
     }
+    bool again = most >= ordered(0x7F800000) || least < ordered(static_cast<int>(0xFF800000));
+    uint64_t stay = ~uint64_t(0);  // groups
     if (grouped) {
       // the two largest choices of every group
-      auto choice = [&](int i) { return BIAS || !sums || key[i] == -kInf ? key[i] : s[i]; };
+      auto choice = [&](int i) { return BIAS || !sums || ord[i] < kLowest ? ord[i] : __float_as_int(s[i]); };
+      auto value = [&](int first, int second) {
+        const float f = __int_as_float(ordered(first));
+        return first < kLowest || (sums && second < kLowest) ? -kInf : sums ? f + __int_as_float(ordered(second)) : f;
+      };
       float* of_group = group_score[wave][slot];
       if (whole) {
-        float first = -kInf, second = -kInf;
+        int first = kOut, second = kOut;
 #pragma unroll
         for (int i = 0; i < V; ++i) merge_one(first, second, choice(i));
-        if (lanes >= 2) merge_two(first, second, dpp<0xB1>(first), dpp<0xB1>(second));
-        if (lanes >= 4) merge_two(first, second, dpp<0x4E>(first), dpp<0x4E>(second));
-        if (lanes >= 8) merge_two(first, second, dpp<0x141>(first), dpp<0x141>(second));
-        if (lanes >= 16) merge_two(first, second, dpp<0x140>(first), dpp<0x140>(second));
-        if ((l & (lanes - 1)) == 0 && e0 < a.E)
-          of_group[e0 / size] = !sums ? first : second == -kInf ? -kInf : first + second;
+        if (lanes >= 2) merge_two(first, second, dpp_int<0xB1>(first), dpp_int<0xB1>(second));
+        if (lanes >= 4) merge_two(first, second, dpp_int<0x4E>(first), dpp_int<0x4E>(second));
+        if (lanes >= 8) merge_two(first, second, dpp_int<0x141>(first), dpp_int<0x141>(second));
+        if (lanes >= 16) merge_two(first, second, dpp_int<0x140>(first), dpp_int<0x140>(second));
+        if ((l & (lanes - 1)) == 0 && (l >> shift) < a.groups) of_group[l >> shift] = value(first, second);
       } else {
-        float* c = narrow[wave][slot];
+        int* c = narrow[wave][slot];
 #pragma unroll
         for (int i = 0; i < V; ++i) c[e0 + i] = choice(i);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         for (int g = l; g < a.groups; g += L) {
-          float first = -kInf, second = -kInf;
+          int first = kOut, second = kOut;
           int at = g % size;  // (groups start at different banks)
           for (int i = 0; i < size; ++i) {
             merge_one(first, second, c[g * size + at]);
             at = at + 1 == size ? 0 : at + 1;
           }
-          of_group[g] = !sums ? first : second == -kInf ? -kInf : first + second;
+          of_group[g] = value(first, second);
         }
       }
+      if (l < 3) of_group[a.groups + l] = -kInf;  // (read below, four at a time)
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       // Groups with fewer than `kept` before them stay.  Maxima of logits compare exactly; of scores and sums the
       // smallest that stays and the largest that does not have to be told apart (equal ones are left to the 64-bit
       // form).
       const bool exact = !BIAS && !sums;
-      uint64_t stay = 0;
+      stay = 0;
       float low = kInf, high = -kInf;
       for (int g0 = 0; g0 < a.groups; g0 += L) {
         const int g = g0 + l;
         const float mine = g < a.groups ? of_group[g] : -kInf;
         int before = 0;
-        for (int o = 0; o < a.groups; ++o) {
-          const float other = of_group[o];
-          before += other > mine || (exact && other == mine && o < g) ? 1 : 0;
+        for (int o = 0; o < a.groups; o += 4) {
+          const f32x4 other = *reinterpret_cast<const f32x4*>(of_group + o);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) before += other[q] > mine || (exact && other[q] == mine && o + q < g) ? 1 : 0;
         }
         const bool keep = mine > -kInf && before < a.kept;
         stay |= of_token(__ballot(keep)) << g0;
@@ -424,10 +442,22 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
         else
           high = fmaxf(high, mine);
       }
-      low = -max_of<L>(-low);
-      high = max_of<L>(high);
-      const float apart = 4.0f * off + 0x1p-22f * fmaxf(fabsf(low), fabsf(high));
-      again |= !exact && ((high > -kInf && !(low - high > apart)) || __popcll(stay) > a.kept);
+      if (!exact) {
+        low = -max_of<L>(-low);
+        high = max_of<L>(high);
+        const float apart = 4.0f * off + 0x1p-22f * fmaxf(fabsf(low), fabsf(high));
+        again |= (high > -kInf && !(low - high > apart)) || __popcll(stay) > a.kept;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    int code[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) code[i] = EXACT ? (ord[i] & ~0xFFFF) | (1023 - (e0 + i)) : (ord[i] & ~15) | (15 - i);
+    if (grouped && whole) {
+      const bool keep = (stay >> (l >> shift & 63)) & 1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) code[i] = keep ? code[i] : kOut;
+    } else if (grouped) {
       int g = e0 / size, next = (g + 1) * size;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -435,17 +465,8 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
           ++g;
           next += size;
         }
-        if (!((stay >> (g & 63)) & 1)) key[i] = -kInf;
+        if (!((stay >> (g & 63)) & 1)) code[i] = kOut;
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    constexpr int kOut = static_cast<int>(0x80000000);
-    int code[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int b = ordered(__float_as_int(key[i]));
-      code[i] = EXACT ? (b & ~0xFFFF) | (1023 - (e0 + i)) : (b & ~15) | (15 - i);
-      if (key[i] == -kInf) code[i] = kOut;
     }
     sort_keys(code);
     // Lane j: the j-th expert; of inexact keys one more than asked for, which may yet change places with the last.
@@ -458,15 +479,15 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       if constexpr (!EXACT) {
         const float c = __int_as_float(ordered(m & ~15));
         const float apart = (BIAS ? 2.0f * off : 0.0f) + 0x1p-17f * fmaxf(fabsf(before), fabsf(c));
-        if (j < found) close |= j > 0 && m != kOut && !(before - c > apart);
+        if (j < found) close |= j > 0 && m >= kLowest && !(before - c > apart);
         if (j == a.k - 1) last = c;
-        if (j == found) again |= m != kOut && !(last - c > apart);  // three of a kind at the border
+        if (j == found) again |= m >= kLowest && !(last - c > apart);  // three of a kind at the border
         before = c;
       }
       if (j == found) break;
       const int from = __ffsll(static_cast<unsigned long long>(of_token(__ballot(code[0] == m)))) - 1;
       const int e = EXACT ? 1023 - (m & 1023) : from * V + 15 - (m & 15);
-      if (l == j) mine = m == kOut ? -1 : e;
+      if (l == j) mine = m >= kLowest ? e : -1;
       const bool moves = l == from;
 #pragma unroll
       for (int i = 0; i < V - 1; ++i) code[i] = moves ? code[i + 1] : code[i];
@@ -628,7 +649,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
     constexpr bool BF16 = decltype(bf16)::value, BIAS = decltype(bias)::value;
     const dim3 narrow = token_blocks((a.T + 3) / 4), half = token_blocks((a.T + 1) / 2), full = token_blocks(a.T),
                block(kWaves * 64);
-    if (a.E <= 64)
+    if (a.E > 64 && a.E <= 256 && a.T <= 512)  // (less code to fetch: one token 6.7 -> 5.1 us)
+      hipLaunchKernelGGL((route_kernel<BF16, BIAS, 64, 4>), full, block, 0, s, a);
+    else if (a.E <= 64)
       hipLaunchKernelGGL((route_kernel<BF16, BIAS, 16, 4>), narrow, block, 0, s, a);
     else if (a.E <= 128)
       hipLaunchKernelGGL((route_kernel<BF16, BIAS, 16, 8>), narrow, block, 0, s, a);

@@ -17,7 +17,7 @@ namespace fp8fg {
 namespace {
 
 constexpr int kFewWaves = 8, kFewRounds = 2;      // 1024 entries: the workgroups of many, or a single small one
-constexpr int kManyWaves = 16, kManyRounds = 8;   // 8192 entries: the most of a single workgroup
+constexpr int kManyWaves = 16, kManyRounds = 5;   // 5120 entries: the most of a single workgroup (more: 16 us against 12)
 constexpr int64_t kFewRun = kFewWaves * kFewRounds * 64, kManyRun = kManyWaves * kManyRounds * 64;
 constexpr int64_t kMostGroups = 1024;             // (longer inputs: longer runs)
 
@@ -220,14 +220,16 @@ hipError_t launch_segments(const SegmentArgs& a, hipStream_t s) {
   }
   int bits = 0;
   while (a.G >> bits) ++bits;
+  // (a single workgroup's wavefronts share the entries evenly)
+  auto shared = [&](int64_t waves) { return (a.n + waves * 64 - 1) / (waves * 64) * waves * 64; };
   if (a.n <= kFewRun) {
-    hipLaunchKernelGGL((place_kernel<kFewWaves, kFewRounds, true>), dim3(1), dim3(kFewWaves * 64), 0, s, a, kFewRun,
-                       bits);
+    hipLaunchKernelGGL((place_kernel<kFewWaves, kFewRounds, true>), dim3(1), dim3(kFewWaves * 64), 0, s, a,
+                       shared(kFewWaves), bits);
     return hipGetLastError();
   }
   if (a.n <= kManyRun) {
-    hipLaunchKernelGGL((place_kernel<kManyWaves, kManyRounds, true>), dim3(1), dim3(kManyWaves * 64), 0, s, a, kManyRun,
-                       bits);
+    hipLaunchKernelGGL((place_kernel<kManyWaves, kManyRounds, true>), dim3(1), dim3(kManyWaves * 64), 0, s, a,
+                       shared(kManyWaves), bits);
     return hipGetLastError();
   }
   const int64_t run = run_length(a.n);
