@@ -56,7 +56,8 @@ int fp8fg_route_experts(const void* logits, int dtype, int64_t T, int64_t E, int
   if (c != FP8FG_OK) return c;
   if (groups < 1 || groups_kept < 1 || groups_kept > groups || (group_terms != 1 && group_terms != 2))
     return FP8FG_ERR_INVALID_ARG;
-  if (groups > fp8fg::kRouteMaxGroups || E % groups != 0 || k > groups_kept * (E / groups)) return FP8FG_ERR_UNSUPPORTED;
+  if (groups > fp8fg::kRouteMaxGroups || E % groups != 0 || k > groups_kept * (E / groups))
+    return FP8FG_ERR_UNSUPPORTED;
   if (groups_kept < groups && group_terms > E / groups) return FP8FG_ERR_UNSUPPORTED;
   if (T == 0) return FP8FG_OK;
   if (!experts || !weights) return FP8FG_ERR_INVALID_ARG;
@@ -201,8 +202,8 @@ int fp4_quant_weight_1x32(const void* w, int w_dtype, int64_t N, int64_t K, int6
 namespace {
 
 // N: columns of y; a gated w has 2N rows.
-int fp4_product(const void* x, const float* sx, int64_t T, const int32_t* row_index, const int32_t* offsets, bool grouped,
-                int64_t G, const uint8_t* w, const uint8_t* sw, void* y, int y_dtype, bool gated, int64_t M, int64_t N,
+int fp4_product(const void* x, const float* sx, int64_t T, const int32_t* row_index, const int32_t* offsets,
+                bool grouped, int64_t G, const uint8_t* w, const uint8_t* sw, void* y, int y_dtype, bool gated, int64_t M, int64_t N,
                 int64_t K, fp8fg_stream_t stream) {
   if (!valid_dtype(y_dtype) || M < 0 || N < 0 || K < 0 || G < 0 || T < 0) return FP8FG_ERR_INVALID_ARG;
   if (M == 0 || N == 0 || G == 0) return FP8FG_OK;

@@ -91,11 +91,12 @@ struct Segment {
   int first, end;     // its tiles
 };
 
-// The segments of 256 experts, four to a lane: their bounds, held to [0, M] and not decreasing within a
-// segment, and the row tiles of ROWS rows before the lane's.
+// The segments of 256 experts, four to a lane: their bounds, held to [0, M], and the row tiles of ROWS rows before the
+// lane's.  rising: no offset is below the one before it; only then are the tiles no more than the host counted.
 template <int ROWS>
 struct SegmentTable {
   int lo[4], hi[4], before, total;
+  bool rising;
 
   __device__ __forceinline__ int tiles(int i) const { return (hi[i] - lo[i] + ROWS - 1) / ROWS; }
   __device__ __forceinline__ void load(const Fp4Args& a, int64_t base) {
@@ -107,8 +108,10 @@ struct SegmentTable {
       v[i] = a.offsets[g < a.G ? g : a.G];
     }
     int sum = 0;
+    bool falls = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      falls |= v[i + 1] < v[i];
       lo[i] = v[i] < 0 ? 0 : (v[i] > M ? M : v[i]);
       hi[i] = v[i + 1] < lo[i] ? lo[i] : (v[i + 1] > M ? M : v[i + 1]);
       if (base + 4 * lane + i >= a.G) hi[i] = lo[i];
@@ -121,6 +124,7 @@ struct SegmentTable {
       if (lane >= d) incl += o;
     }
     before = incl - sum;
+    rising = __ballot(falls) == 0;
     total = __builtin_amdgcn_readlane(incl, 63);
   }
   // The segment of tile t, numbered from the table's first; false: it lies behind the table.
@@ -215,11 +219,14 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
   if constexpr (GROUPED) {
     table.load(a, 0);
     row_tiles = table.total;
+    bool rising = table.rising;
     for (int64_t base = 256; base < a.G; base += 256) {
       SegmentTable<XR> more;
       more.load(a, base);
       row_tiles += more.total;
+      rising &= more.rising;
     }
+    if (!rising) return;
   }
   const int all = row_tiles * col_tiles;
   const int each = uniform(all / static_cast<int>(gridDim.x)), rest = all - each * static_cast<int>(gridDim.x);
@@ -284,7 +291,8 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
 #pragma unroll
     for (int i = 0; i < WD; ++i) {
       const int p = 64 * i + lane, r = p / WC;
-      w_off[i] = static_cast<uint32_t>((w_row(r / 16, r % 16) - n0) * (a.K / 2)) + (place<WC>(r, p % WC) - r * WC) * 16;
+      w_off[i] =
+          static_cast<uint32_t>((w_row(r / 16, r % 16) - n0) * (a.K / 2)) + (place<WC>(r, p % WC) - r * WC) * 16;
     }
 #pragma unroll
     for (int i = 0; i < SD; ++i) {
@@ -462,7 +470,8 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
       }
       if (u % 4 == 0 && stage > 0) r_slot = r_slot == SS - 1 ? 0 : r_slot + 1;
       ++stage;
-      multiply(u, ring + w_slot * W_STAGE, ring + S_AT + r_slot * S_STAGE + (u % 4) * (KU / 32), ring + X_AT + x_slot * X_STAGE);
+      multiply(u, ring + w_slot * W_STAGE, ring + S_AT + r_slot * S_STAGE + (u % 4) * (KU / 32),
+               ring + X_AT + x_slot * X_STAGE);
       w_slot = w_slot == SW - 1 ? 0 : w_slot + 1;
       x_slot = x_slot == SX - 1 ? 0 : x_slot + 1;
     }

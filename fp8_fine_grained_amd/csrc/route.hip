@@ -280,8 +280,8 @@ __device__ __forceinline__ void merge_two(int& first, int& second, int f, int s)
 //    rounding of a score are put in order by their 64-bit values.  Where that does not do (three in one place at the
 //    border, sums of groups that lie close) the token is done again in 64 bits, and so is one with a value that is not
 //    a number or +infinity.
-// Bound by the instructions of its rounds and their fetch, not by the logits' bytes (8192 x 256 fp32 in 8 groups 12.2 us,
-// 1.7 for the bytes), so four tokens of up to 256 experts share a wavefront: a round costs the same for one.  (A
+// Bound by the instructions of its rounds and their fetch, not by the logits' bytes (8192 x 256 fp32 in 8 groups: 12.2
+// us, 1.7 for the bytes), so four tokens of up to 256 experts share a wavefront: a round costs the same for one.  (A
 // wavefront per token, all in 64 bits: 83 us.)
 template <bool BF16, bool BIAS, int L, int V>
 __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {

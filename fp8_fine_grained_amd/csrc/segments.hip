@@ -17,7 +17,7 @@ namespace fp8fg {
 namespace {
 
 constexpr int kFewWaves = 8, kFewRounds = 2;      // 1024 entries: the workgroups of many, or a single small one
-constexpr int kManyWaves = 16, kManyRounds = 5;   // 5120 entries: the most of a single workgroup (more: 16 us against 12)
+constexpr int kManyWaves = 16, kManyRounds = 5;   // 5120 entries: the most of a single workgroup (8192: 16 us, not 12)
 constexpr int64_t kFewRun = kFewWaves * kFewRounds * 64, kManyRun = kManyWaves * kManyRounds * 64;
 constexpr int64_t kMostGroups = 1024;             // (longer inputs: longer runs)
 

@@ -199,8 +199,8 @@ int fp4_gated_gemm(const void* x, const float* sx, const uint8_t* w, const uint8
  * w, sw        codes [G, N, K/2] and scales [G, N, K/32]  (gated: N = 2I).
  * y, h         out, [M_total, N] or [M_total, I], in routed-row order.  Rows behind
  *              group_offsets[G] stay as they were.
- * Offsets that decrease or pass M_total, and indices outside [0, T), are held to them:
- * unspecified rows, never an access outside the operands.
+ * Offsets below 0 or above M_total, and indices outside [0, T), are held to these; with
+ * offsets that decrease nothing is written.  Never an access outside the operands.
  * Requires G < 2^31, (M_total + 2 * min(G, M_total)) * (N + 8) < 2^35, and with row_index an X of
  * less than 4 GiB; otherwise as above.
  */

@@ -95,6 +95,24 @@ def test_two_calls_at_once_on_two_streams(gpu):
                 assert all(torch.equal(a, b) for a, b in zip(want, leaves)), name
 
 
+def test_every_call_in_a_graph(gpu):
+    """Replayed several times, with the program's own eager calls and waits between: the eager results each time."""
+    for name, call in _calls(gpu):
+        want = _leaves(call())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = _leaves(call())
+        for _ in range(3):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            eager = _leaves(call())
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got)), name
+            assert all(torch.equal(a, b) for a, b in zip(want, eager)), name
+
+
 # ------------------------------------------------------------------ a layer in FP8 and in 4 bits
 class Weights:
     def __init__(self, gpu, E, H, inner, seed=0):

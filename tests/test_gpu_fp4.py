@@ -253,8 +253,35 @@ def test_offsets_and_indices_that_break_the_rules_stay_inside(gpu):
     for bad in ([-3, 4, 2, 50, 9], [9, 0, 0, 0, 0], [0, 2 ** 31 - 1, 5, -2 ** 31, 9], [5, 5, 5, 5, 5]):
         room = torch.full((9 + 8, 48), 7.0, device=gpu)
         ex.fp4_grouped_gemm(xs, torch.tensor(bad, dtype=torch.int32, device=gpu), ws, sws, y=room[4:13])
-        torch.cuda.synchronize()
-        assert torch.all(room[:4] == 7) and torch.all(room[13:] == 7)
+        assert torch.all(room == 7), bad
+    # rising offsets beyond the rows are held to them
+    room = torch.full((9 + 8, 48), 7.0, device=gpu)
+    o = torch.tensor([-2 ** 31, -5, 4, 2 ** 31 - 1, 2 ** 31 - 1], dtype=torch.int32, device=gpu)
+    ex.fp4_grouped_gemm(xs, o, ws, sws, y=room[4:13])
+    v = ref.x_values(x)
+    assert torch.equal(room[4:8].cpu().double(), v[:4] @ ref.fp4_values(w[1], sw[1]).t())
+    assert torch.equal(room[8:13].cpu().double(), v[4:] @ ref.fp4_values(w[2], sw[2]).t())
+    assert torch.all(room[:4] == 7) and torch.all(room[13:] == 7)
+
+
+def test_offsets_of_many_experts_that_fall_somewhere(gpu):
+    """Every expert's segment whole but for one that falls: the tiles would be more than the launch counts on."""
+    G = 700
+    x, _, w, sw = exact_operands(300, 48, 128, False, G=G)
+    xs, ws, sws = on(gpu, x, w, sw)
+    for where in (1, 255, 256, 257, 511, 512, 699):
+        offsets = torch.full((G + 1,), 300, dtype=torch.int32)
+        offsets[0], offsets[where] = 0, 0
+        y = torch.full((300, 48), 7.0, device=gpu)
+        ex.fp4_grouped_gemm(xs, offsets.to(gpu), ws, sws, y=y)
+        if where == 1:  # (rises: the second expert has all rows)
+            assert torch.equal(y.cpu().double(), ref.x_values(x) @ ref.fp4_values(w[1], sw[1]).t())
+        else:
+            assert torch.all(y == 7), where
+    zigzag = torch.tensor([0, 300] * 351, dtype=torch.int32)[:G + 1]
+    y = torch.full((300, 48), 7.0, device=gpu)
+    ex.fp4_grouped_gemm(xs, zigzag.to(gpu), ws, sws, y=y)
+    assert torch.all(y == 7)
 
 
 def test_every_code_and_scale(gpu):
