@@ -4,7 +4,9 @@ FP8 GEMM for AMD MI355X (gfx950).
 The product is the C-ABI library ``libfp8fg.so`` (include/fp8fg.h) built from
 ``csrc/``; :mod:`fp8_fine_grained_amd.binding` calls it from Python with
 torch tensors as device memory, and :mod:`fp8_fine_grained_amd.layer` the
-operators between the GEMMs (include/fp8fg_layer.h).  The seeded synthetic inputs come from the
+operators between the GEMMs (include/fp8fg_layer.h), and
+:mod:`fp8_fine_grained_amd.experts` those around the grouped GEMMs of an expert
+layer and the 4-bit weights (include/fp8fg_experts.h).  The seeded synthetic inputs come from the
 top-level ``workloads`` module, outside this package.
 """
 

@@ -203,8 +203,8 @@ namespace {
 
 // N: columns of y; a gated w has 2N rows.
 int fp4_product(const void* x, const float* sx, int64_t T, const int32_t* row_index, const int32_t* offsets,
-                bool grouped, int64_t G, const uint8_t* w, const uint8_t* sw, void* y, int y_dtype, bool gated, int64_t M, int64_t N,
-                int64_t K, fp8fg_stream_t stream) {
+                bool grouped, int64_t G, const uint8_t* w, const uint8_t* sw, void* y, int y_dtype, bool gated,
+                int64_t M, int64_t N, int64_t K, fp8fg_stream_t stream) {
   if (!valid_dtype(y_dtype) || M < 0 || N < 0 || K < 0 || G < 0 || T < 0) return FP8FG_ERR_INVALID_ARG;
   if (M == 0 || N == 0 || G == 0) return FP8FG_OK;
   if (K == 0 || K % 128 != 0 || K >= (int64_t(1) << 24) || M > kInt32Max || N > kInt32Max || G > kInt32Max ||

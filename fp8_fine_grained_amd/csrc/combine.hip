@@ -1,7 +1,8 @@
 // Combination of the experts' rows and its gradient.
 //     y[t] = base[t] + sum_j w[t, j] * rows[p[t, j]]             (fp32, in the order of j)
 //     drows[p[t, j]] = w[t, j] * dy[t],  dw[t, j] = <dy[t], rows[p[t, j]]>
-// Bound by HBM: every row is read (and written) once.
+// Bound by HBM: every row is read (and written) once.  8192 tokens of 8 x 7168 bf16: 211 us (5.6 TB/s, most of it
+// read), the gradient with quantised rows 317 us (4.9 TB/s, read and written).
 #include <type_traits>
 
 #include "launch.h"
@@ -120,7 +121,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a, int64_
 
 // W wavefronts per token take the pieces in turn, J places at a time, so that dy is read once for all of them and J
 // rows' loads are in flight; the dot products' parts meet in LDS, in the order of the wavefronts.  One wavefront does
-// for short rows (100000 tokens of 2 x 256, quantised: 311 -> 68 us), sixteen share few tokens (one of 8 x 7168: 8.5 -> 5.5 us).
+// for short rows (100000 tokens of 2 x 256, quantised: 311 -> 68 us), sixteen share few tokens (one of 8 x 7168: 8.5
+// -> 5.5 us).
 // DW: dweights are asked for (the rows are read).
 template <bool BF16, bool QUANT, bool DW, int J, int W>
 __global__ void __launch_bounds__(W == 1 ? kThreads : W * 64) combine_backward_kernel(CombineGradArgs a) {

@@ -1,7 +1,9 @@
 // 4-bit weights: their quantisation (E2M1 codes, one power-of-two scale per 32 elements along
 // K) and products of few rows with them, dense or over expert segments, plain or gated:
 //     y = x W^T,   or  h = g * sigmoid(g) * u  with g, u the two halves of x W^T.
-// Bound by the stream of the weights from HBM (4.25 bits each).
+// Bound by the stream of the weights from HBM (4.25 bits each) for up to 16 rows: 36864 x 7168 with one row 30 us, at
+// 4.7 TB/s; 29 experts of 4096 x 7168 with 128 rows 97 us, at the same rate.  With more rows of X by what a tile costs a
+// wavefront: its instructions that widen W, and X's way through L2 and LDS (48 rows, 7168 x 18432: 36-39 us, 1.9 TB/s).
 //
 // The products run on the bf16 matrix cores: every E2M1 value times its power of two, and
 // every E4M3 value, is a bf16 value, so each product is exact and the sums are fp32.

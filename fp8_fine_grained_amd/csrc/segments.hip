@@ -9,6 +9,8 @@
 // entries per expert, and each workgroup of the second sums the table (all of it for the
 // segments' starts, the rows before its own for its own).
 // Entries of no local expert form a last bin of their own behind the segments.
+// Bound by its dependent steps, not by its few bytes: 8 entries take 3.7 us, 65536 over 256 experts 4 us to count
+// and 8 us to place.
 #include <type_traits>
 
 #include "launch.h"
