@@ -215,7 +215,7 @@ int fp4_product(const void* x, const float* sx, int64_t T, const int32_t* row_in
   // The weights' bytes are counted in 64 bits, tiles in 31, lanes' offsets (from a tile's gate rows to its up
   // rows, from the first token to the last) in 32.
   if (G > kInt64Max / 2 / (gated ? 2 : 1) / N / K) return FP8FG_ERR_UNSUPPORTED;
-  for (const fp8fg::Fp4Shape& s : fp8fg::kFp4Shapes)
+  for (const fp8fg::Fp4Shape& s : fp8fg::kFp4Shapes[sx != nullptr])
     if (fp8fg::fp4_tiles(M, N, G, grouped, gated, s) > kInt32Max) return FP8FG_ERR_UNSUPPORTED;
   if (gated && (N + 128) * (K / 2) > kUint32Max) return FP8FG_ERR_UNSUPPORTED;
   if (grouped && row_index && T * K * (sx ? 1 : 2) > kUint32Max) return FP8FG_ERR_UNSUPPORTED;

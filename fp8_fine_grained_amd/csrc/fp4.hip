@@ -1,9 +1,9 @@
 // 4-bit weights: their quantisation (E2M1 codes, one power-of-two scale per 32 elements along
 // K) and products of few rows with them, dense or over expert segments, plain or gated:
 //     y = x W^T,   or  h = g * sigmoid(g) * u  with g, u the two halves of x W^T.
-// Bound by the stream of the weights from HBM (4.25 bits each) for up to 16 rows: 36864 x 7168 with one row 30 us, at
-// 4.7 TB/s; 29 experts of 4096 x 7168 with 128 rows 97 us, at the same rate.  With more rows of X by what a tile costs a
-// wavefront: its instructions that widen W, and X's way through L2 and LDS (48 rows, 7168 x 18432: 36-39 us, 1.9 TB/s).
+// Bound by the stream of the weights from HBM (4.25 bits each) for up to 16 rows: 36864 x 7168 with one row 31 us, at
+// 4.5 TB/s; 29 experts of 4096 x 7168 with 128 rows 96 us, at 4.7.  With more rows of X by what a tile costs a
+// wavefront: its instructions that widen W, and X's way through L2 and LDS (48 rows, 7168 x 18432: 34-36 us, 2.0 TB/s).
 //
 // The products run on the bf16 matrix cores: every E2M1 value times its power of two, and
 // every E4M3 value, is a bf16 value, so each product is exact and the sums are fp32.
@@ -182,6 +182,13 @@ __device__ __forceinline__ void wait_last(int left) {
   }
 }
 
+// Sub-tiles whose partial sums a wavefront puts into `room` KB at a time: a divisor of all of them.
+constexpr int sums_at_once(int all, int room) {
+  int n = all;
+  while (n > room || all % n != 0) --n;
+  return n;
+}
+
 // A workgroup walks over tiles of XR rows of X by NF sub-tiles of 16 rows of W (gated: 8 gate
 // rows and the 8 up rows of the same columns).  Its KW wavefronts take a part of K each; every
 // wavefront moves its own operands, KU values of K at a time, into rings of its own in LDS (SW
@@ -205,10 +212,11 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
   constexpr int WAIT = later_loads(LX, LW, SX, SW, SW - 1);
   constexpr int W_STAGE = WD * 1024, X_STAGE = XD * 1024 + SXD * 256, S_STAGE = SD * 256, SS = SW;
   constexpr int S_AT = SW * W_STAGE, X_AT = S_AT + SS * S_STAGE;
-  constexpr int RING = X_AT + SX * X_STAGE, RED = KW * MF * NF * 1024;
+  constexpr int RING = X_AT + SX * X_STAGE;
+  constexpr int SUMS = sums_at_once(MF * NF, WD + XD);
   static_assert(SW >= SX && WAIT < 64, "the wait counter");
-  static_assert(KW * RING + RED <= 163840, "LDS");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[KW * RING + RED];
+  static_assert(KW * RING <= 163840, "LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KW * RING];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, j = lane >> 4;
   const int KB = static_cast<int>(a.K / 128);
@@ -232,7 +240,11 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
   }
   const int all = row_tiles * col_tiles;
   const int each = uniform(all / static_cast<int>(gridDim.x)), rest = all - each * static_cast<int>(gridDim.x);
-  const int block = static_cast<int>(blockIdx.x);
+  // workgroups of one XCD (every eighth) take neighbouring tiles: those of the same columns of W share its L2
+  // (512 rows over 32 experts of 4096 x 7168: 151 -> 140 us; 48 rows, 7168 x 18432: 38 -> 34)
+  const int xcd = static_cast<int>(blockIdx.x) & 7, grid = static_cast<int>(gridDim.x);
+  const int block =
+      xcd * (grid >> 3) + (xcd < (grid & 7) ? xcd : grid & 7) + (static_cast<int>(blockIdx.x) >> 3);
   const int t0 = block * each + (block < rest ? block : rest), t1 = t0 + each + (block < rest ? 1 : 0);
   if (t0 >= t1) return;
   auto locate = [&](int t, Segment& s, int& lo, int& hi, int& n0) {
@@ -452,7 +464,15 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
       if (cw.stage < stages) issue_w();
     }
   }
-  f32x4(*sums)[MF * NF][64] = reinterpret_cast<f32x4(*)[MF * NF][64]>(lds + KW * RING);
+  // Where a wavefront v's partial sums of sub-tile q lie: in the slots that it has read last, which are not loaded into
+  // before its next stage.  (Room of their own, and with it one barrier's wait less, is no faster, and the room is
+  // better spent on longer stages: 16 rows of 7168 x 18432 24.3 -> 21.5 us.)
+  auto sums_of = [&](int v, int q, int tiles) -> f32x4* {
+    const uint32_t nv = (v + 1) * NU / KW - v * NU / KW, n = tiles;  // (a wavefront without stages: any slot)
+    uint8_t* own = lds + v * RING;
+    return reinterpret_cast<f32x4*>(q < WD ? own + (n % SW * nv + SW - 1) % SW * W_STAGE + q * 1024
+                                           : own + X_AT + (n % SX * nv + SX - 1) % SX * X_STAGE + (q - WD) * 1024);
+  };
   int w_slot = 0, x_slot = 0, r_slot = 0;
   int64_t stage = 0;
   for (int t = t0; t < t1; ++t) {
@@ -477,46 +497,55 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
       w_slot = w_slot == SW - 1 ? 0 : w_slot + 1;
       x_slot = x_slot == SX - 1 ? 0 : x_slot + 1;
     }
-    // (the sums of the tile before have been read)
-    if (t > t0) asm volatile("s_barrier" ::: "memory");
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-      for (int f = 0; f < NF; ++f) sums[wave][m * NF + f][lane] = acc[m][f];
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     int lo, hi, n0;
     locate(t, sc, lo, hi, n0);
+    const int tiles = t - t0 + 1;
 #pragma unroll
-    for (int r = 0; r < MF * NF; ++r) {
-      if (r % KW != wave) continue;
-      f32x4 y = sums[0][r][lane];
+    for (int r0 = 0; r0 < MF * NF; r0 += SUMS) {
 #pragma unroll
-      for (int v = 1; v < KW; ++v) y += sums[v][r][lane];
-      // lane: row `row` of W's sub-tile, rows 4j .. 4j + 3 of X's
-      const int64_t m0 = static_cast<int64_t>(lo) + 16 * (r / NF) + 4 * j;
-      const int64_t c = static_cast<int64_t>(n0) + (GATED ? (r % NF) * 8 + (row & 7) : (r % NF) * 16 + row);
+      for (int q = 0; q < SUMS; ++q) sums_of(wave, q, tiles)[lane] = acc[(r0 + q) / NF][(r0 + q) % NF];
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      constexpr int MINE = (SUMS + KW - 1) / KW;
+      f32x4 total[MINE];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v = y[i];
-        if constexpr (GATED) {
-          const float up = __shfl_xor(v, 8);
-          v = v * sigmoid(v) * up;
+      for (int i = 0; i < MINE; ++i) {
+        const int q = i * KW + wave;
+        total[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (q >= SUMS) continue;
+#pragma unroll
+        for (int v = 0; v < KW; ++v) total[i] += sums_of(v, q, tiles)[lane];
+      }
+      // (the sums have been read: the slots may be written again)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int r = r0 + i * KW + wave;
+        if (r >= r0 + SUMS) continue;
+        // lane: row `row` of W's sub-tile, rows 4j .. 4j + 3 of X's
+        const int64_t m0 = static_cast<int64_t>(lo) + 16 * (r / NF) + 4 * j;
+        const int64_t c = static_cast<int64_t>(n0) + (GATED ? (r % NF) * 8 + (row & 7) : (r % NF) * 16 + row);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v = total[i][k];
+          if constexpr (GATED) {
+            const float up = __shfl_xor(v, 8);
+            v = v * sigmoid(v) * up;
+          }
+          if (m0 + k >= hi || c >= a.N || (GATED && row >= 8)) continue;
+          const int64_t at = (m0 + k) * a.N + c;
+          if (a.y_bf16)
+            static_cast<uint16_t*>(a.y)[at] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+          else
+            static_cast<float*>(a.y)[at] = v;
         }
-        if (m0 + i >= hi || c >= a.N || (GATED && row >= 8)) continue;
-        const int64_t at = (m0 + i) * a.N + c;
-        if (a.y_bf16)
-          static_cast<uint16_t*>(a.y)[at] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
-        else
-          static_cast<float*>(a.y)[at] = v;
       }
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
 template <bool CODES, bool GATED, bool GROUPED, int I>
 hipError_t launch_shape(const Fp4Args& a, int shape, hipStream_t s) {
-  constexpr Fp4Shape t = kFp4Shapes[I];
+  constexpr Fp4Shape t = kFp4Shapes[CODES][I];
   if (shape == I) {
     const int64_t tiles = fp4_tiles(a.M, a.N, a.G, a.offsets != nullptr, a.gated, t);
     const int cus = device_cus();
@@ -531,7 +560,7 @@ hipError_t launch_shape(const Fp4Args& a, int shape, hipStream_t s) {
 
 int shape_of(const Fp4Args& a) {
   const int cus = device_cus();
-  return choose_fp4_shape(a.M, a.N, a.G, a.offsets != nullptr, a.gated, cus > 0 ? cus : 256);
+  return choose_fp4_shape(a.M, a.N, a.G, a.offsets != nullptr, a.gated, a.sx != nullptr, cus > 0 ? cus : 256);
 }
 
 }  // namespace

@@ -16,10 +16,10 @@ SOURCE = """
 using namespace fp8fg;
 int main(int argc, char** argv) {
   printf("%d\\n", kFp4ShapeCount);
-  for (int i = 1; i + 4 < argc; i += 5) {
+  for (int i = 1; i + 5 < argc; i += 6) {
     const int64_t M = atoll(argv[i]), N = atoll(argv[i + 1]), G = atoll(argv[i + 2]);
-    const bool grouped = atoi(argv[i + 3]) != 0, gated = atoi(argv[i + 4]) != 0;
-    printf("%d\\n", choose_fp4_shape(M, N, G, grouped, gated, 256));
+    const bool grouped = atoi(argv[i + 3]) != 0, gated = atoi(argv[i + 4]) != 0, codes = atoi(argv[i + 5]) != 0;
+    printf("%d\\n", choose_fp4_shape(M, N, G, grouped, gated, codes, 256));
   }
 }
 """
@@ -38,17 +38,19 @@ def choose(tmp_path_factory):
     return run
 
 
-def test_the_gpu_tests_take_every_shape_in_every_form(choose):
+@pytest.mark.parametrize("codes", [False, True])
+def test_the_gpu_tests_take_every_shape_in_every_form(choose, codes):
     for gated in (False, True):
-        count, dense = choose(*[(M, N // 2 if gated else N, 1, False, gated) for M, N in SHAPED])
+        count, dense = choose(*[(M, N // 2 if gated else N, 1, False, gated, codes) for M, N in SHAPED])
         assert sorted(set(dense)) == list(range(count)), (gated, dense)
         # over two segments, one of them empty, the estimate halves the rows: other shapes, still most of them
-        _, grouped = choose(*[(M, N // 2 if gated else N, 2, True, gated) for M, N in SHAPED])
+        _, grouped = choose(*[(M, N // 2 if gated else N, 2, True, gated, codes) for M, N in SHAPED])
         assert len(set(grouped)) >= 8, (gated, grouped)
 
 
 def test_choices(choose):
-    _, got = choose((1, 4096, 1, False, False), (1, 2048, 1, False, True), (8, 4096, 1, False, False),
-                    (16, 4096, 1, False, False), (64, 7168, 1, False, False), (128, 2048, 32, True, True),
-                    (8, 2048, 256, True, True))
-    assert got == [0, 0, 3, 5, 10, 4, 2]
+    _, got = choose((1, 4096, 1, False, False, False), (1, 2048, 1, False, True, False),
+                    (5, 7168, 1, False, False, True), (8, 4096, 1, False, False, False), (16, 4096, 1, False, False, False),
+                    (32, 7168, 1, False, False, True), (64, 7168, 1, False, False, False),
+                    (128, 2048, 32, True, True, False), (8, 2048, 256, True, True, False))
+    assert got == [0, 0, 4, 3, 6, 10, 11, 5, 2]
