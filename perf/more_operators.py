@@ -159,7 +159,7 @@ def _plan(gen, T, k, drop):
     choice = torch.rand((T, max(2 * k, 16)), generator=gen, device="cuda").argsort(dim=1)[:, :k].flatten()
     n = choice.numel()
     gone = torch.randperm(n, generator=gen, device="cuda") < int(drop * n)
-    order = (choice + gone * n).argsort(stable=True)
+    order = (choice + gone * max(n, 2 * k, 16)).argsort(stable=True)  # (dropped ones behind every kept one)
     positions = torch.empty_like(choice)
     positions[order] = torch.arange(n, device="cuda")
     return torch.where(gone, -1, positions).to(torch.int32).view(T, k), n - int(drop * n)
