@@ -100,7 +100,7 @@ struct SegmentTable {
   int lo[4], hi[4], before, total;
   bool rising;
 
-  __device__ __forceinline__ int tiles(int i) const { return (hi[i] - lo[i] + ROWS - 1) / ROWS; }
+  __device__ __forceinline__ int tiles(int i) const { return fp4_row_tiles(lo[i], hi[i], ROWS); }
   __device__ __forceinline__ void load(const Fp4Args& a, int64_t base) {
     const int lane = threadIdx.x & 63, M = static_cast<int>(a.M);
     int v[5];
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(KW * 64) fp4_gemm_kernel(Fp4Args a) {
         }
       }
     }
-    const int rt = (s.hi - s.lo + XR - 1) / XR, r = t - s.first, c = rt == 1 ? r : uniform(r / rt);
+    const int rt = fp4_row_tiles(s.lo, s.hi, XR), r = t - s.first, c = rt == 1 ? r : uniform(r / rt);
     lo = s.lo + (r - c * rt) * XR;
     hi = s.hi - lo > XR ? lo + XR : s.hi;
     n0 = c * COLS;

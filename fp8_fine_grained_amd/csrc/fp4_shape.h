@@ -40,6 +40,12 @@ constexpr Fp4Shape kFp4Shapes[2][kFp4ShapeCount] = {
      {32, 2, 4, 4, 2, 256, 0.158f},
      {32, 4, 8, 2, 2, 128, 0.245f}}};
 
+// Tiles of `rows` rows that cover rows lo .. hi - 1, lo <= hi.  (Unsigned: hi - lo may be up to 2^31 - 1.)
+constexpr int fp4_row_tiles(int lo, int hi, int rows) {
+  return static_cast<int>((static_cast<uint32_t>(hi) - static_cast<uint32_t>(lo) + static_cast<uint32_t>(rows - 1)) /
+                          static_cast<uint32_t>(rows));
+}
+
 // Tiles of a launch; over segments an upper bound.
 inline int64_t fp4_tiles(int64_t M, int64_t N, int64_t G, bool grouped, bool gated, const Fp4Shape& s) {
   const int64_t cols = (gated ? 8 : 16) * s.nf;
