@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
   __shared__ double wide[kWaves][L * V];             // of tokens that are done again
   __shared__ int narrow[kWaves][TOKENS][L * V];    // choices, where groups lie across lanes
   __shared__ __attribute__((aligned(16))) float group_score[kWaves][TOKENS][kRouteMaxGroups + 4];
+  __shared__ float group_off[kWaves][TOKENS][kRouteMaxGroups];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (L - 1), slot = lane / L;
   const int e0 = l * V;
@@ -393,7 +394,13 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
         const float f = __int_as_float(ordered(first));
         return first < kLowest || (sums && second < kLowest) ? -kInf : sums ? f + __int_as_float(ordered(second)) : f;
       };
+      // How far it may be off: its terms' scores, their roundings (a term may be far larger than the sum) and the sum's.
+      auto error = [&](int first, int second) {
+        const float f = 0x1p-23f * fabsf(__int_as_float(ordered(first)));
+        return 2.0f * off + (sums ? fmaf(0x1p-23f, fabsf(__int_as_float(ordered(second))), f) : f);
+      };
       float* of_group = group_score[wave][slot];
+      float* off_group = group_off[wave][slot];
       if (whole) {
         int first = kOut, second = kOut;
 #pragma unroll
@@ -402,7 +409,10 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
         if (lanes >= 4) merge_two(first, second, dpp_int<0x4E>(first), dpp_int<0x4E>(second));
         if (lanes >= 8) merge_two(first, second, dpp_int<0x141>(first), dpp_int<0x141>(second));
         if (lanes >= 16) merge_two(first, second, dpp_int<0x140>(first), dpp_int<0x140>(second));
-        if ((l & (lanes - 1)) == 0 && (l >> shift) < a.groups) of_group[l >> shift] = value(first, second);
+        if ((l & (lanes - 1)) == 0 && (l >> shift) < a.groups) {
+          of_group[l >> shift] = value(first, second);
+          off_group[l >> shift] = error(first, second);
+        }
       } else {
         int* c = narrow[wave][slot];
 #pragma unroll
@@ -416,16 +426,17 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
             at = at + 1 == size ? 0 : at + 1;
           }
           of_group[g] = value(first, second);
+          off_group[g] = error(first, second);
         }
       }
       if (l < 3) of_group[a.groups + l] = -kInf;  // (read below, four at a time)
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       // Groups with fewer than `kept` before them stay.  Maxima of logits compare exactly; of scores and sums the
-      // smallest that stays and the largest that does not have to be told apart (equal ones are left to the 64-bit
-      // form).
+      // least that one that stays may be has to lie above the most that one that does not may be (equal ones are left
+      // to the 64-bit form).
       const bool exact = !BIAS && !sums;
       stay = 0;
-      float low = kInf, high = -kInf;
+      float low = kInf;
       for (int g0 = 0; g0 < a.groups; g0 += L) {
         const int g = g0 + l;
         const float mine = g < a.groups ? of_group[g] : -kInf;
@@ -437,16 +448,21 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
         }
         const bool keep = mine > -kInf && before < a.kept;
         stay |= of_token(__ballot(keep)) << g0;
-        if (keep)
-          low = fminf(low, mine);
-        else
-          high = fmaxf(high, mine);
+        if (keep) low = fminf(low, mine);
       }
       if (!exact) {
         low = -max_of<L>(-low);
-        high = max_of<L>(high);
-        const float apart = 4.0f * off + 0x1p-22f * fmaxf(fabsf(low), fabsf(high));
-        again |= (high > -kInf && !(low - high > apart)) || __popcll(stay) > a.kept;
+        float staying = kInf, leaving = -kInf;  // (above `low`: differences at the border are exact)
+        for (int g = l; g < a.groups; g += L) {
+          const float d = of_group[g] - low;
+          if ((stay >> g) & 1)
+            staying = fminf(staying, d - off_group[g]);
+          else
+            leaving = fmaxf(leaving, d + off_group[g]);
+        }
+        staying = -max_of<L>(-staying);
+        leaving = max_of<L>(leaving);
+        again |= (leaving > -kInf && !(staying > leaving)) || __popcll(stay) > a.kept;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
