@@ -391,8 +391,11 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
       // the two largest choices of every group
       auto choice = [&](int i) { return BIAS || !sums || ord[i] < kLowest ? ord[i] : __float_as_int(s[i]); };
       auto value = [&](int first, int second) {
-        const float f = __int_as_float(ordered(first));
-        return first < kLowest || (sums && second < kLowest) ? -kInf : sums ? f + __int_as_float(ordered(second)) : f;
+        float v = __int_as_float(ordered(first));
+        if (first < kLowest || (sums && second < kLowest)) return -kInf;
+        if (sums) v += __int_as_float(ordered(second));
+        again |= fabsf(v) == kInf;  // (a sum past fp32's range is no reason to leave a group out)
+        return v;
       };
       // How far it may be off: its terms' scores, their roundings (a term may be far larger than the sum) and the sum's.
       auto error = [&](int first, int second) {

@@ -1,5 +1,5 @@
 """Groups of experts whose sums of two choices fp32 cannot tell apart, because the terms are far larger than their sum or
-than the scores in them: the groups that stay are those of the real numbers."""
+than the scores in them, or cannot hold: the groups that stay are those of the real numbers."""
 
 import pytest
 import torch
@@ -26,6 +26,24 @@ def test_sums_whose_terms_cancel(gpu, E, groups, score, dtype):
         for T0 in (T, 40):  # (few tokens take another shape of the kernel)
             check(gpu, z[:T0], min(6, E // 2), (B, T0), bias=bias.flatten(), score=score, groups=groups,
                   groups_kept=groups // 2, group_terms=2)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups", SIZES)
+def test_sums_that_fp32_cannot_hold(gpu, E, groups, score):
+    """Biases of the type's lowest and largest value: sums of two lie past its range, and such groups are there
+    all the same."""
+    size, kept = E // groups, groups // 2
+    z = _logits(600, E, torch.float32, seed=E + 1)
+    low = torch.finfo(torch.float32).min
+    for value in (low, -2.0e38, -low):
+        bias = torch.full((groups, size), value)
+        bias[1], bias[-1] = 0.0, 0.01
+        for T in (600, 40):
+            for k in {min(12, 3 * size), 2}:
+                if k <= kept * size:
+                    check(gpu, z[:T], k, (value, T, k), bias=bias.flatten(), score=score, groups=groups,
+                          groups_kept=kept, group_terms=2)
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
