@@ -23,4 +23,20 @@ __device__ __forceinline__ float sigmoid(float g) {
   return fmaf(fmaf(-x, r, 1.0f), r, r);
 }
 
+// s = 1 / (1 + exp(-g)) and c = 1 - s = 1 / (1 + exp(g)), each to about an ulp of its own, from one
+// exponential: with e = exp(-|g|) the one is 1 / (1 + e) and the other e / (1 + e).
+__device__ __forceinline__ void sigmoid_and_rest(float g, float& s, float& c) {
+  constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147181f;
+  const float a = fminf(fabsf(g), 100.0f);
+  const float hi = -a * kLog2e;
+  const float lo = fmaf(-a, kLog2e, -hi) - a * kLog2eRest;
+  float e = __builtin_amdgcn_exp2f(hi);
+  e = fmaf(e, lo * kLn2, e);
+  const float x = 1.0f + e;
+  float r = __builtin_amdgcn_rcpf(x);
+  r = fmaf(fmaf(-x, r, 1.0f), r, r);
+  s = g < 0.0f ? e * r : r;
+  c = g < 0.0f ? r : e * r;
+}
+
 }  // namespace fp8fg

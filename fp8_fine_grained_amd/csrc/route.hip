@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_kernel(RouteArgs a) {
         again |= fabsf(v) == kInf;  // (a sum past fp32's range is no reason to leave a group out)
         return v;
       };
-      // How far it may be off: its terms' scores, their roundings (a term may be far larger than the sum) and the sum's.
+      // How far it may be off: its terms' scores, their roundings (a term may be far above the sum), the sum's.
       auto error = [&](int first, int second) {
         const float f = 0x1p-23f * fabsf(__int_as_float(ordered(first)));
         return 2.0f * off + (sums ? fmaf(0x1p-23f, fabsf(__int_as_float(ordered(second))), f) : f);
@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_backward_kernel(RouteGradAr
     int mine = lane < a.k ? a.experts[t * a.k + lane] : -1;
     float dw = lane < a.k ? a.dw[t * a.k + lane] : 0.0f;
     float z[STEPS], s[STEPS], d[STEPS];
+    float rest[STEPS];  // 1 - s of the sigmoid: a confident expert's is far below the rounding of s
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
       const int e = lane + 64 * i;
@@ -596,7 +597,11 @@ __global__ void __launch_bounds__(kWaves * 64) route_backward_kernel(RouteGradAr
     float top = out, total = 1.0f;
     if (a.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) s[i] = score(z[i]);
+      for (int i = 0; i < STEPS; ++i) {
+        sigmoid_and_rest(z[i], s[i], rest[i]);
+        if (z[i] == out) s[i] = 0.0f;
+        if (z[i] != z[i]) s[i] = rest[i] = z[i];
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) top = fmaxf(top, z[i]);
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(kWaves * 64) route_backward_kernel(RouteGradAr
     for (int i = 0; i < STEPS; ++i) {
       const int e = lane + 64 * i;
       if (e >= a.E) continue;
-      float v = a.sigmoid ? d[i] * (1.0f - s[i]) : d[i] - s[i] * u;
+      float v = a.sigmoid ? d[i] * rest[i] : d[i] - s[i] * u;
       if (z[i] == out) v = 0.0f;
       if constexpr (BF16)
         static_cast<uint16_t*>(a.dz)[t * a.E + e] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
