@@ -132,12 +132,14 @@ int combine_backward(const void* dy, const void* rows, int dtype, int64_t R, int
   int c = check_combine(dtype, R, H, T, k);
   if (c != FP8FG_OK) return c;
   if (T == 0 || k == 0) return FP8FG_OK;
-  if (!positions || (!drows && !dweights) || (R > 0 && dweights && !rows)) return FP8FG_ERR_INVALID_ARG;
-  if (!aligned(positions, 4) || !aligned(weights, 4) || !aligned(scales, 4) || !aligned(dweights, 4) ||
-      !aligned(drows, 16))
+  const bool any = R > 0 && H > 0;  // (rows and their gradient without elements may have no address)
+  if (!positions || (any && ((!drows && !dweights) || (dweights && !rows)))) return FP8FG_ERR_INVALID_ARG;
+  if (!aligned(positions, 4) || !aligned(weights, 4) || !aligned(dweights, 4) ||
+      (any && (!aligned(scales, 4) || !aligned(drows, 16))))
     return FP8FG_ERR_MISALIGNED;
   if (H > 0 && (c = check_rows(dy, dtype, T, H, ld_dy)) != FP8FG_OK) return c;
-  if (H > 0 && R > 0 && dweights && (c = check_rows(rows, dtype, R, H, ld_rows)) != FP8FG_OK) return c;
+  if (any && dweights && (c = check_rows(rows, dtype, R, H, ld_rows)) != FP8FG_OK) return c;
+  if (!any && !dweights) return FP8FG_OK;
   fp8fg::CombineGradArgs a{};
   a.dy = dy; a.rows = rows; a.positions = positions; a.weights = weights; a.drows = drows; a.scales = scales;
   a.dw = dweights; a.R = R; a.H = H; a.ld_dy = ld_dy; a.ld_rows = ld_rows; a.T = T; a.k = static_cast<int>(k);

@@ -131,7 +131,8 @@ int fp8fg_combine_experts(const void* rows, int dtype, int64_t R, int64_t H, int
  * weights      fp32 [T, k], or NULL (ones).
  * drows        out, [R, H] of `dtype`, or NULL.  Rows that no position names stay as they
  *              were.
- * dweights     out, fp32 [T, k], or NULL.  One of both has to be asked for.
+ * dweights     out, fp32 [T, k], or NULL.  One of both has to be asked for; where R == 0 or H == 0,
+ *              rows and drows have no elements and are not looked at (dweights are 0).
  * Requirements as the forward call's.
  */
 int fp8fg_combine_experts_backward(const void* dy, const void* rows, int dtype, int64_t R, int64_t H, int64_t ld_dy,
