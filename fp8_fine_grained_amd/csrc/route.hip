@@ -123,14 +123,15 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
     total = wave_sum(total);
   }
   // what experts are ranked by (score: also without a bias)
+  auto bias = [&](int e) { return a.bias ? static_cast<double>(a.bias[e]) : 0.0; };
+  auto score_of = [&](int e) {
+    const double z = logit(e), f = a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - top);
+    return a.sigmoid || f == 0.0 ? f : f / total;
+  };
   auto rank = [&](int e, bool score) -> double {
-    const float z = logit(e), b = a.bias ? a.bias[e] : 0.0f;
-    if (z == outf || b == outf) return out;
-    double c = z;
-    if (score || a.bias) {
-      const double f = a.sigmoid ? 1.0 / (1.0 + exp(-c)) : exp(c - top);
-      c = (a.sigmoid || f == 0.0 ? f : f / total) + static_cast<double>(b);
-    }
+    const double z = logit(e), b = bias(e);
+    if (z == out || b == out) return out;
+    const double c = score || a.bias ? score_of(e) + b : z;
     return c == c ? c : kNotANumber;
   };
   uint64_t stay = ~uint64_t(0);
@@ -146,11 +147,36 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, doubl
         first = fmax(first, v);
       }
     }
-    const double score = a.terms == 1 ? first : second == out ? out : first + second;
-    int before = 0;  // groups that come before this lane's
-    for (int g = 0; g < a.groups; ++g) {
-      const double o = __shfl(score, g);
-      if (o > score || (o == score && g < lane)) ++before;
+    double score = a.terms == 1 ? first : second == out ? out : first + second;
+    const bool sum = a.terms == 2 && a.bias && second > kNotANumber && score < -out;
+    // how far the sums' roundings may bring two of them
+    const double apart = 0x1p-49 * max_of<64>(sum ? static_cast<float>(fabs(first) + fabs(second)) : 0.0f);
+    int before;  // groups that come before this lane's
+    bool close;
+    auto compare = [&]() {
+      before = 0;
+      close = false;
+      for (int g = 0; g < a.groups; ++g) {
+        const double o = __shfl(score, g);
+        if (o > score || (o == score && g < lane)) ++before;
+        close |= g != lane && fabs(o - score) <= apart;
+      }
+      close &= sum;
+    };
+    compare();
+    if (__ballot(close)) {
+      // Scores and biases for themselves: sums that tie as real numbers are equal whichever bias goes with which score.
+      if (sum) {
+        int at = -1, next = -1;
+        for (int e = lane * size; e < (lane + 1) * size; ++e) {
+          if (at < 0 && value[e] == first)
+            at = e;
+          else if (value[e] == second)
+            next = e;
+        }
+        score = (score_of(at) + score_of(next)) + (bias(at) + bias(next));
+      }
+      compare();
     }
     stay = __ballot(lane < a.groups && before < a.kept && score != out);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
