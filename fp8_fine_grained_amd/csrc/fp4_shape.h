@@ -12,7 +12,8 @@ struct Fp4Shape {
   float per_block;
 };
 // Of X in bf16, and in E4M3 codes, whose smaller stages leave 32 rows of X twice as long ones or twice the
-// wavefronts (7168 x 18432, 32 rows: 30.6 -> 27.8 us; 48 rows: 39 -> 34).
+// wavefronts (7168 x 18432, 32 rows: 30.6 -> 27.8 us; 48 rows: 39 -> 34).  Up to 16 rows both types
+// take the same times.
 constexpr int kFp4ShapeCount = 12;
 constexpr Fp4Shape kFp4Shapes[2][kFp4ShapeCount] = {
     {{2, 1, 8, 4, 4, 256, 0.054f},

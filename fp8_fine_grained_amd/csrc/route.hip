@@ -14,7 +14,7 @@
 namespace fp8fg {
 namespace {
 
-constexpr int kWaves = 4;                       // tokens of a workgroup
+constexpr int kWaves = 4;                       // wavefronts of a workgroup
 constexpr int64_t kMostBlocks = int64_t(1) << 20;
 constexpr int kSteps = kRouteMaxE / 64;         // experts of a lane: lane, lane + 64, ...
 constexpr double kNotANumber = -1e300;          // ranks below every fp32 number, above what is out

@@ -1,5 +1,5 @@
-"""Groups of experts whose sums of two choices fp32 cannot tell apart, because the terms are far larger than their sum or
-than the scores in them, or cannot hold: the groups that stay are those of the real numbers."""
+"""Groups of experts whose sums of two choices fp32 cannot tell apart, because the terms are far larger than their sum
+or than the scores in them, or cannot hold: the groups that stay are those of the real numbers."""
 
 import pytest
 import torch
